@@ -1,4 +1,4 @@
-"""ctypes binding of libtpconv.so (include/tpconv.h).
+"""ctypes binding of libtpconv.so (include/tpconv.h, tpconv_graph.h, tpconv_node.h).
 
 Argument marshalling only: every computation runs in the library's kernels.  Tensors
 are torch tensors (device memory, float32 / int32, contiguous); PyTorch is used to
@@ -17,6 +17,7 @@ BESSEL, GAUSSIAN = 0, 1
 PASS_FORWARD, PASS_BACKWARD, PASS_DOUBLE_BACKWARD = 1, 2, 4
 MATH_FP32, MATH_TF32, MATH_BF16 = 0, 1, 2
 LAYOUT_IR_MUL, LAYOUT_MUL_IR = 0, 1
+DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 
 _c_i64 = ctypes.c_int64
 _c_p = ctypes.c_void_p
@@ -25,6 +26,11 @@ _c_p = ctypes.c_void_p
 class RadialSpec(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("num_basis", ctypes.c_int32), ("r_cut", ctypes.c_float),
                 ("r_min", ctypes.c_float), ("r_max", ctypes.c_float), ("poly_p", ctypes.c_int32)]
+
+
+class DropoutSpec(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("step", ctypes.c_void_p)]
 
 
 # symbol -> (restype, argtypes); mirrors include/tpconv.h
@@ -60,8 +66,22 @@ SIGNATURES = {
     "tpconv_spatial_order": (ctypes.c_int, [_c_i64, _c_p, _c_p, _c_p, ctypes.c_size_t, _c_p]),
     "tpconv_permute_graph": (ctypes.c_int, [_c_i64, _c_i64] + [_c_p] * 6 + [_c_p]),
     "tpconv_gather_rows": (ctypes.c_int, [_c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p]),
+    # include/tpconv_node.h
+    "tpconv_node_plan_create": (ctypes.c_int, [ctypes.POINTER(_c_p), ctypes.c_char_p, ctypes.c_int32,
+                                               ctypes.c_float]),
+    "tpconv_node_plan_destroy": (ctypes.c_int, [_c_p]),
+    "tpconv_node_plan_info": (ctypes.c_int, [_c_p] + [ctypes.POINTER(_c_i64)] * 4),
+    "tpconv_node_plan_set_layout": (ctypes.c_int, [_c_p, ctypes.c_int32]),
+    "tpconv_node_workspace_bytes": (ctypes.c_int, [_c_p, _c_i64, ctypes.POINTER(ctypes.c_size_t)]),
+    "tpconv_norm_forward": (ctypes.c_int, [_c_p, _c_i64] + [_c_p] * 5),
+    "tpconv_norm_backward": (ctypes.c_int, [_c_p, _c_i64] + [_c_p] * 7 + [ctypes.c_size_t, _c_p]),
+    "tpconv_norm_double_backward": (ctypes.c_int, [_c_p, _c_i64] + [_c_p] * 10 + [ctypes.c_size_t, _c_p]),
+    "tpconv_dropout_forward": (ctypes.c_int, [_c_p, _c_i64] + [_c_p] * 5),
+    "tpconv_dropout_backward": (ctypes.c_int, [_c_p, _c_i64] + [_c_p] * 4),
+    "tpconv_dropout_norm_forward": (ctypes.c_int, [_c_p, _c_i64] + [_c_p] * 8),
+    "tpconv_dropout_norm_backward": (ctypes.c_int, [_c_p, _c_i64] + [_c_p] * 10 + [ctypes.c_size_t, _c_p]),
 }
-PROF_CATEGORIES = 13
+PROF_CATEGORIES = 14
 
 _lib = None
 
@@ -375,6 +395,257 @@ def tpconv_gather_rows(a, perm, stream=None):
     check(lib().tpconv_gather_rows(perm.numel(), width, _ptr(a), _ptr(perm), _ptr(out), _stream(stream)),
           "tpconv_gather_rows")
     return out
+
+
+# ---------------------------------------------------------------------------
+# node-feature operators (include/tpconv_node.h)
+# ---------------------------------------------------------------------------
+
+class NodePlan:
+    """tpconv_node_plan_create / _destroy: rows of an irreps string in a storage type
+    (torch.float32, bfloat16 or float16), the norm's eps and the layout ("ir_mul" or
+    "mul_ir", or the LAYOUT_ constants)."""
+
+    def __init__(self, irreps, dtype=None, eps=1e-5, layout=LAYOUT_IR_MUL):
+        import torch
+        dtype = torch.float32 if dtype is None else dtype
+        codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+        if dtype not in codes:
+            raise ValueError(f"dtype must be one of {sorted(map(str, codes))}")
+        if isinstance(layout, str):
+            if layout not in ("ir_mul", "mul_ir"):
+                raise ValueError("layout must be 'ir_mul' or 'mul_ir'")
+            layout = LAYOUT_MUL_IR if layout == "mul_ir" else LAYOUT_IR_MUL
+        h = _c_p()
+        check(lib().tpconv_node_plan_create(ctypes.byref(h), irreps.encode(), codes[dtype], float(eps)),
+              "tpconv_node_plan_create")
+        self._h = h
+        self.dtype, self.eps = dtype, float(eps)
+        vals = [_c_i64() for _ in range(4)]
+        check(lib().tpconv_node_plan_info(h, *[ctypes.byref(v) for v in vals]), "tpconv_node_plan_info")
+        self.dim, self.channels, self.biases, self.num_blocks = (v.value for v in vals)
+        self.set_layout(layout)
+
+    @property
+    def handle(self):
+        return self._h
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().tpconv_node_plan_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def set_layout(self, layout):
+        """LAYOUT_IR_MUL (blocks [2l+1][C]) or LAYOUT_MUL_IR (blocks [C][2l+1])."""
+        check(lib().tpconv_node_plan_set_layout(self._h, int(layout)), "tpconv_node_plan_set_layout")
+
+    def workspace_bytes(self, n_rows):
+        """Workspace of norm and dropout-norm backward and of the double backward."""
+        out = ctypes.c_size_t()
+        check(lib().tpconv_node_workspace_bytes(self._h, int(n_rows), ctypes.byref(out)),
+              "tpconv_node_workspace_bytes")
+        return out.value
+
+
+class Dropout:
+    """tpconv_dropout_spec: probability p of dropping, seed, offset (one per layer and step) and
+    an optional device int64 ``step`` that the kernels add to the offset when they run."""
+
+    def __init__(self, p, seed, offset=0, step=None):
+        import torch
+        if not 0.0 <= float(p) <= 1.0:
+            raise ValueError("p must be in [0, 1]")
+        if step is not None:
+            _need(step, torch.int64, "step")
+            if step.numel() != 1:
+                raise ValueError("step must hold one value")
+        self.step = step            # kept alive with the spec
+        self._spec = DropoutSpec(float(p), int(seed) & (2 ** 64 - 1), int(offset) & (2 ** 64 - 1),
+                                 None if step is None else step.data_ptr())
+        self._ref = ctypes.byref(self._spec)
+
+    @property
+    def p(self):
+        return self._spec.p
+
+    @property
+    def seed(self):
+        return self._spec.seed
+
+    @property
+    def offset(self):
+        return self._spec.offset
+
+    @offset.setter
+    def offset(self, value):
+        self._spec.offset = int(value) & (2 ** 64 - 1)
+
+
+def _node_rows(plan, device, *arrays):
+    """Rows N of node arrays ((tensor, name), the first one required), all [N, dim] in the plan's
+    type, on one device."""
+    N = None
+    for t, name in arrays:
+        if t is None:
+            if N is None:
+                raise ValueError(f"{name} is required")
+            continue
+        _need(t, plan.dtype, name)
+        if t.dim() != 2 or t.shape[1] != plan.dim:
+            raise ValueError(f"{name} must have {plan.dim} columns")
+        if N is None:
+            N = t.shape[0]
+        if t.shape[0] != N:
+            raise ValueError(f"{name} must have {N} rows")
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}")
+    return N
+
+
+def _node_params(device, *arrays):
+    """Channel vectors: (tensor or None, length, name)."""
+    import torch
+    for t, n, name in arrays:
+        if t is None:
+            continue
+        _need(t, torch.float32, name)
+        if t.numel() != n:
+            raise ValueError(f"{name} must have {n} values")
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}")
+
+
+def _node_call(device, name, stream, *args):
+    """One library call on the tensors' device and the given (or that device's current) stream."""
+    import torch
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _node_call(device, name, stream, *args)
+    check(getattr(lib(), name)(*args, _stream(stream)), name)
+
+
+def _node_ws(plan, N, ws, device):
+    if ws is None:
+        return workspace(plan.workspace_bytes(N), device)
+    if not ws.is_cuda or ws.device != device:
+        raise ValueError(f"ws must be on {device}")
+    return ws
+
+
+def tpconv_norm_forward(plan, x, weight=None, bias=None, out=None, stream=None):
+    """Irreps layer norm of node rows x [N, dim]; weight [channels], bias [biases] float32."""
+    import torch
+    dev = x.device
+    if out is None:
+        out = torch.empty_like(x)
+    N = _node_rows(plan, dev, (x, "x"), (out, "out"))
+    _node_params(dev, (weight, plan.channels, "weight"), (bias, plan.biases, "bias"))
+    _node_call(dev, "tpconv_norm_forward", stream, plan.handle, N, _ptr(x), _ptr(weight), _ptr(bias), _ptr(out))
+    return out
+
+
+def tpconv_norm_backward(plan, x, weight, grad_y, need_x=True, need_weight=True, need_bias=True, ws=None,
+                         outputs=None, stream=None):
+    """Returns (grad_x [N, dim], grad_weight [channels], grad_bias [biases])."""
+    import torch
+    dev = x.device
+    if outputs is None:
+        gx = torch.empty_like(x) if need_x else None
+        gw = torch.empty(plan.channels, dtype=torch.float32, device=dev) if need_weight else None
+        gb = torch.empty(plan.biases, dtype=torch.float32, device=dev) if need_bias else None
+    else:
+        gx, gw, gb = outputs
+    N = _node_rows(plan, dev, (x, "x"), (grad_y, "grad_y"), (gx, "grad_x"))
+    _node_params(dev, (weight, plan.channels, "weight"), (gw, plan.channels, "grad_weight"),
+                 (gb, plan.biases, "grad_bias"))
+    ws = _node_ws(plan, N, ws, dev)
+    _node_call(dev, "tpconv_norm_backward", stream, plan.handle, N, _ptr(x), _ptr(weight), _ptr(grad_y), _ptr(gx),
+               _ptr(gw), _ptr(gb), _ptr(ws), ws.numel() * ws.element_size())
+    return gx, gw, gb
+
+
+def tpconv_norm_double_backward(plan, x, weight, grad_y, gg_x=None, gg_weight=None, gg_bias=None, need_x=True,
+                                need_weight=True, need_grad_y=True, ws=None, outputs=None, stream=None):
+    """Returns (grad_x [N, dim], grad_weight [channels], grad_grad_y [N, dim])."""
+    import torch
+    dev = x.device
+    if outputs is None:
+        gx = torch.empty_like(x) if need_x else None
+        gw = torch.empty(plan.channels, dtype=torch.float32, device=dev) if need_weight else None
+        gg = torch.empty_like(x) if need_grad_y else None
+    else:
+        gx, gw, gg = outputs
+    N = _node_rows(plan, dev, (x, "x"), (grad_y, "grad_y"), (gg_x, "gg_x"), (gx, "grad_x"), (gg, "grad_grad_y"))
+    _node_params(dev, (weight, plan.channels, "weight"), (gg_weight, plan.channels, "gg_weight"),
+                 (gg_bias, plan.biases, "gg_bias"), (gw, plan.channels, "grad_weight"))
+    ws = _node_ws(plan, N, ws, dev)
+    _node_call(dev, "tpconv_norm_double_backward", stream, plan.handle, N, _ptr(x), _ptr(weight), _ptr(grad_y),
+               _ptr(gg_x), _ptr(gg_weight), _ptr(gg_bias), _ptr(gx), _ptr(gw), _ptr(gg), _ptr(ws),
+               ws.numel() * ws.element_size())
+    return gx, gw, gg
+
+
+def tpconv_dropout_forward(plan, x, dropout, residual=None, out=None, stream=None):
+    """residual + dropout(x); ``dropout`` is a Dropout.  out may be x or residual (in place)."""
+    import torch
+    dev = x.device
+    if out is None:
+        out = torch.empty_like(x)
+    N = _node_rows(plan, dev, (x, "x"), (residual, "residual"), (out, "out"))
+    _node_call(dev, "tpconv_dropout_forward", stream, plan.handle, N, _ptr(x), _ptr(residual), dropout._ref, _ptr(out))
+    return out
+
+
+def tpconv_dropout_backward(plan, grad_out, dropout, out=None, stream=None):
+    """grad_x of tpconv_dropout_forward (the residual's gradient is grad_out itself)."""
+    import torch
+    dev = grad_out.device
+    if out is None:
+        out = torch.empty_like(grad_out)
+    N = _node_rows(plan, dev, (grad_out, "grad_out"), (out, "out"))
+    _node_call(dev, "tpconv_dropout_backward", stream, plan.handle, N, _ptr(grad_out), dropout._ref, _ptr(out))
+    return out
+
+
+def tpconv_dropout_norm_forward(plan, x, dropout, residual=None, weight=None, bias=None, outputs=None, stream=None):
+    """Returns (z, y): z = residual + dropout(x), y = norm(z)."""
+    import torch
+    dev = x.device
+    z, y = (torch.empty_like(x), torch.empty_like(x)) if outputs is None else outputs
+    N = _node_rows(plan, dev, (x, "x"), (z, "z"), (y, "y"), (residual, "residual"))
+    _node_params(dev, (weight, plan.channels, "weight"), (bias, plan.biases, "bias"))
+    _node_call(dev, "tpconv_dropout_norm_forward", stream, plan.handle, N, _ptr(x), _ptr(residual), dropout._ref,
+               _ptr(weight), _ptr(bias), _ptr(z), _ptr(y))
+    return z, y
+
+
+def tpconv_dropout_norm_backward(plan, z, weight, grad_y, dropout, grad_z=None, need_x=True, need_residual=True,
+                                 need_weight=True, need_bias=True, ws=None, outputs=None, stream=None):
+    """Returns (grad_x, grad_residual, grad_weight, grad_bias) from the stored z."""
+    import torch
+    dev = z.device
+    if outputs is None:
+        gx = torch.empty_like(z) if need_x else None
+        gr = torch.empty_like(z) if need_residual else None
+        gw = torch.empty(plan.channels, dtype=torch.float32, device=dev) if need_weight else None
+        gb = torch.empty(plan.biases, dtype=torch.float32, device=dev) if need_bias else None
+    else:
+        gx, gr, gw, gb = outputs
+    N = _node_rows(plan, dev, (z, "z"), (grad_y, "grad_y"), (grad_z, "grad_z"), (gx, "grad_x"),
+                   (gr, "grad_residual"))
+    _node_params(dev, (weight, plan.channels, "weight"), (gw, plan.channels, "grad_weight"),
+                 (gb, plan.biases, "grad_bias"))
+    ws = _node_ws(plan, N, ws, dev)
+    _node_call(dev, "tpconv_dropout_norm_backward", stream, plan.handle, N, _ptr(z), _ptr(weight), _ptr(grad_y),
+               _ptr(grad_z), dropout._ref, _ptr(gx), _ptr(gr), _ptr(gw), _ptr(gb), _ptr(ws),
+               ws.numel() * ws.element_size())
+    return gx, gr, gw, gb
 
 
 def tpconv_profile_begin(max_records=8192):

@@ -24,16 +24,16 @@
 #include <mutex>
 
 #include "../../include/tpconv.h"
+#include "irreps.h"
 #include "launch.h"
+#include "prof.h"
 #include "tables.inc"
 
 using namespace tpc;
 
-namespace {
+static_assert(TPC_LMAX == kMaxOrder, "generated tables and irreps parser agree on the largest order");
 
-struct Block {
-  int mul, l, parity, offset;
-};
+namespace {
 
 struct PathH {
   int l_in, l_sh, l_out, b_in, b_out, c_in, c_out, w_off, w_count, type, nnz;
@@ -79,62 +79,18 @@ void cg_of_type(int type, std::vector<int>& idx, std::vector<double>& val) {
   }
 }
 
-tpconv_status parse_irreps(const char* s, std::vector<Block>& out) {
-  if (!s) return TPCONV_ERR_INVALID_ARG;
-  out.clear();
-  std::string str(s);
-  size_t pos = 0;
-  int off = 0;
-  if (str.find_first_not_of(" \t") == std::string::npos) return TPCONV_ERR_PARSE;
-  while (pos <= str.size()) {
-    size_t plus = str.find('+', pos);
-    std::string tok = str.substr(pos, plus == std::string::npos ? std::string::npos : plus - pos);
-    std::string t;
-    for (char ch : tok) if (ch != ' ' && ch != '\t') t.push_back(ch);
-    if (t.empty()) return TPCONV_ERR_PARSE;
-    long mul = 1;
-    size_t xp = t.find('x');
-    std::string lp = t;
-    if (xp != std::string::npos) {
-      std::string ms = t.substr(0, xp);
-      if (ms.empty() || ms.find_first_not_of("0123456789") != std::string::npos || ms.size() > 6) return TPCONV_ERR_PARSE;
-      mul = std::atol(ms.c_str());
-      lp = t.substr(xp + 1);
-    }
-    if (lp.size() < 2) return TPCONV_ERR_PARSE;
-    char par = lp.back();
-    std::string ls = lp.substr(0, lp.size() - 1);
-    if ((par != 'e' && par != 'o') || ls.empty() || ls.find_first_not_of("0123456789") != std::string::npos || ls.size() > 3)
-      return TPCONV_ERR_PARSE;
-    long l = std::atol(ls.c_str());
-    if (mul <= 0) return TPCONV_ERR_PARSE;
-    if (l > TPC_LMAX) return TPCONV_ERR_UNSUPPORTED;
-    Block b{(int)mul, (int)l, par == 'e' ? 1 : -1, off};
-    off += b.mul * (2 * b.l + 1);
-    out.push_back(b);
-    if (plus == std::string::npos) break;
-    pos = plus + 1;
-  }
-  if ((int)out.size() > MAX_BLOCKS) return TPCONV_ERR_UNSUPPORTED;
-  return TPCONV_OK;
-}
-
 inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // ---------------------------------------------------------------------------
 // profiling: optional CUDA-event bracketing of every kernel launch, by category
 // ---------------------------------------------------------------------------
 
-enum ProfCat {
-  PC_UVW_STATE = 0, PC_UVW_STATE_TAN, PC_UVW_RECV_BWD, PC_UVW_SRC, PC_UVW_SRC_TAN, PC_GEMM,
-  PC_UVU_FWD, PC_UVU_RECV_BWD, PC_UVU_GRADW, PC_UVU_SRC, PC_POS, PC_GRAPH, PC_RECV_TAN, PC_COUNT
-};
 static_assert(PC_COUNT == TPCONV_PROF_CATEGORIES, "category count");
 const char* const kProfNames[PC_COUNT] = {
     "uvw_receiver_state", "uvw_receiver_state_tangent", "uvw_receiver_backward", "uvw_source_state",
     "uvw_source_state_tangent", "channel_gemm", "uvu_forward", "uvu_receiver_backward",
     "uvu_weight_gradient", "uvu_source_backward", "position_gradient", "graph",
-    "receiver_backward_tangent"};
+    "receiver_backward_tangent", "node_features"};
 
 struct Prof {
   std::mutex mu;
@@ -156,27 +112,23 @@ void prof_add_launches(int c, int n) {
   if (P.on) P.launches[c] += n;
 }
 
-// Brackets one library call that launches `nk` kernels on stream s.
-struct ProfScope {
-  int slot = -1;
-  cudaStream_t s;
-  ProfScope(int c, int nk, cudaStream_t st) : s(st) {
-    Prof& P = prof();
-    std::lock_guard<std::mutex> g(P.mu);
-    if (!P.on) return;
-    P.launches[c] += nk;
-    if (2 * (P.used + 1) > P.pool.size()) return;
-    slot = (int)P.used++;
-    P.cat[slot] = c;
-    cudaEventRecord(P.pool[2 * slot], s);
-  }
-  ~ProfScope() {
-    if (slot < 0) return;
-    cudaEventRecord(prof().pool[2 * slot + 1], s);
-  }
-};
-
 }  // namespace
+
+int tpc::prof_open(int c, int nk, cudaStream_t s) {
+  Prof& P = prof();
+  std::lock_guard<std::mutex> g(P.mu);
+  if (!P.on) return -1;
+  P.launches[c] += nk;
+  if (2 * (P.used + 1) > P.pool.size()) return -1;
+  const int slot = (int)P.used++;
+  P.cat[slot] = c;
+  cudaEventRecord(P.pool[2 * slot], s);
+  return slot;
+}
+
+void tpc::prof_close(int slot, cudaStream_t s) {
+  if (slot >= 0) cudaEventRecord(prof().pool[2 * slot + 1], s);
+}
 
 struct tpconv_plan {
   std::vector<Block> in, out;

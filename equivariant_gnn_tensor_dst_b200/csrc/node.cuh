@@ -1,0 +1,58 @@
+// Device helpers of the node-feature kernels: storage types, the dropout generator, sums.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "node.h"
+
+namespace tpc {
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <class T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+// Philox4x32-10: ten rounds of two 32 x 32 -> 64 products on a 128-bit counter, the key
+// advanced by fixed odd increments (Salmon et al. 2011, section 4.3).
+__device__ __forceinline__ uint4 philox10(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t k0,
+                                          uint32_t k1) {
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
+    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+    c1 = (uint32_t)b;
+    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+    c3 = (uint32_t)a;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return make_uint4(c0, c1, c2, c3);
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4& w, int i) {
+  return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
+}
+
+// offset + *step of a call
+__device__ __forceinline__ uint64_t drop_offset(const Drop& D) {
+  return D.offset + (D.step ? (uint64_t)*D.step : 0ull);
+}
+
+// Words of a row's channel group.
+__device__ __forceinline__ uint4 drop_words(const Drop& D, uint64_t off, uint32_t group, uint32_t row) {
+  return philox10(group, row, (uint32_t)off, (uint32_t)(off >> 32), D.k0, D.k1);
+}
+
+// kept ? v * scale : 0 for one channel, drawing its group's words
+__device__ __forceinline__ float drop_one(const Drop& D, uint64_t off, const NodeBlock& B, int c, uint32_t row,
+                                          float v) {
+  if (D.mode == 0) return v;
+  if (D.mode == 2) return 0.f;
+  const uint4 w = drop_words(D, off, B.grp0 + (c >> 2), row);
+  return word_of(w, c & 3) >= D.threshold ? v * D.scale : 0.f;
+}
+
+}  // namespace tpc

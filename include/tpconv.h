@@ -282,7 +282,7 @@ tpconv_status tpconv_forward_no_alloc(tpconv_plan_t plan, int64_t N, int64_t E, 
  * total device milliseconds and launch counts into ms[n] / launches[n] (either may be
  * NULL; n <= TPCONV_PROF_CATEGORIES) and disables recording.  Not for use during
  * stream capture.                                                                     */
-#define TPCONV_PROF_CATEGORIES 13
+#define TPCONV_PROF_CATEGORIES 14
 
 /* Reads and clears the library's device error word (0 = fine; nonzero = a bounded wait
  * inside a tensor-core kernel gave up, so results of that launch are invalid).
