@@ -23,7 +23,8 @@ _PARTS = {"STATE": 1, "SRC": 2, "RECV": 3, "FWD": 4, "GRADW": 5}
 
 def _units():
     units = [("k_misc.cu", {}), ("k_gemm_tc.cu", {}), ("launch.cu", {}), ("api.cu", {}), ("k_order.cu", {}),
-             ("k_norm.cu", {}), ("k_dropout.cu", {}), ("node_api.cu", {})]
+             ("node_api.cu", {})]
+    units += [("k_node.cu", {"TPC_UNIT_T": t}) for t in (0, 1, 2)]   # storage types
     for kp in (8, 16):
         for mode in (0, 1):   # generic and fast variants of the receiver backward
             units.append(("k_recv_edge.cu", {"TPC_UNIT_KP": kp, "TPC_UNIT_MODE": mode}))

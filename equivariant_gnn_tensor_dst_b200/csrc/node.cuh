@@ -52,7 +52,39 @@ __device__ __forceinline__ float drop_one(const Drop& D, uint64_t off, const Nod
   if (D.mode == 0) return v;
   if (D.mode == 2) return 0.f;
   const uint4 w = drop_words(D, off, B.grp0 + (c >> 2), row);
-  return word_of(w, c & 3) >= D.threshold ? v * D.scale : 0.f;
+  return word_of(w, c & 3) >= D.threshold ? __fmul_rn(v, D.scale) : 0.f;
+}
+
+// V consecutive elements, loaded and stored in one access.
+template <class T, int V>
+struct alignas(sizeof(T) * V) Pack {
+  T v[V];
+};
+
+// Which channels of a block the elements s (block-relative) belong to.
+struct Channels {
+  int mul_ir, C, d;
+  uint32_t inv;  // ceil(2^32 / (mul_ir ? d : C)): exact quotients for s, C < 2^15
+  __device__ __forceinline__ Channels(const NodeDesc& D, const NodeBlock& B) : mul_ir(D.mul_ir), C(B.C), d(B.d) {
+    const uint32_t q = mul_ir ? d : C;
+    inv = q > 1 ? (uint32_t)((0x100000000ull + q - 1) / q) : 0;
+  }
+  __device__ __forceinline__ int of(int s) const {
+    if (mul_ir) return d == 1 ? s : (int)__umulhi((uint32_t)s, inv);
+    return C == 1 ? 0 : s - C * (int)__umulhi((uint32_t)s, inv);
+  }
+  __device__ __forceinline__ int at(int c, int m) const { return mul_ir ? c * d + m : m * C + c; }
+};
+
+// Sums of K values over groups of G lanes (a power of two, at most 32), to all lanes of a group.
+template <int K>
+__device__ __forceinline__ void group_sum(float (&v)[K], int G) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (G > o) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    }
 }
 
 }  // namespace tpc

@@ -57,7 +57,7 @@ enum NormPass { NORM_FORWARD = 0, NORM_BACKWARD = 1, NORM_DOUBLE_BACKWARD = 2 };
 // drop != NULL: the fused dropout + residual variants of forward and backward.
 cudaError_t launch_norm(NormPass pass, int dtype, const NodeDesc& D, long long N, const NormArgs& A, const Drop* drop,
                         cudaStream_t s);
-size_t norm_partial_floats(const NodeDesc& D, long long N);
+size_t norm_partial_floats(const NodeDesc& D, long long N, int esize);  // elements of esize bytes
 cudaError_t launch_dropout(int dtype, const NodeDesc& D, long long N, const void* x, const void* residual,
                            const Drop& drop, void* out, cudaStream_t s);
 

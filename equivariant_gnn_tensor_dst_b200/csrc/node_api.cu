@@ -73,7 +73,7 @@ tpconv_status make_drop(const tpconv_dropout_spec* spec, Drop& d) {
 // Bytes of the workspace that a pass writes, for the overlap check (one that is too small is
 // reported as that).
 size_t ws_span(const tpconv_node_plan* P, int64_t N, size_t ws_bytes) {
-  const size_t need = sizeof(float) * norm_partial_floats(P->desc, N);
+  const size_t need = sizeof(float) * norm_partial_floats(P->desc, N, (int)elem_bytes(P));
   return ws_bytes < need ? ws_bytes : need;
 }
 
@@ -82,7 +82,9 @@ tpconv_status sums_workspace(const tpconv_node_plan* P, int64_t N, bool wanted, 
                              float** partial) {
   *partial = nullptr;
   if (!wanted || N == 0) return TPCONV_OK;
-  if (ws_bytes < sizeof(float) * norm_partial_floats(P->desc, N)) return TPCONV_ERR_WORKSPACE_TOO_SMALL;
+  const size_t need = sizeof(float) * norm_partial_floats(P->desc, N, (int)elem_bytes(P));
+  if (ws_bytes < need) return TPCONV_ERR_WORKSPACE_TOO_SMALL;
+  if (need == 0) return TPCONV_OK;  // few rows: the sums go to the gradients themselves
   if (!ws) return TPCONV_ERR_INVALID_ARG;
   *partial = static_cast<float*>(ws);
   return TPCONV_OK;
@@ -167,7 +169,7 @@ tpconv_status tpconv_node_plan_set_layout(tpconv_node_plan_t P, int32_t layout) 
 
 tpconv_status tpconv_node_workspace_bytes(tpconv_node_plan_t P, int64_t N, size_t* bytes) {
   if (!bytes || !rows_ok(P, N)) return TPCONV_ERR_INVALID_ARG;
-  *bytes = sizeof(float) * norm_partial_floats(P->desc, N);
+  *bytes = sizeof(float) * norm_partial_floats(P->desc, N, (int)elem_bytes(P));
   return TPCONV_OK;
 }
 

@@ -250,7 +250,7 @@ def test_64_bit_offsets(torch):
 
 def test_binding_checks(torch):
     from equivariant_gnn_tensor_dst_b200 import binding as B
-    p = Problem(MIXED, 10)
+    p = Problem(MIXED, 5000)
     gy, _ = p.rows()
     for bad in (lambda: B.tpconv_norm_forward(p.plan, p.x[:, :100]), lambda: B.tpconv_norm_forward(p.plan, p.x.half()),
                 lambda: B.tpconv_norm_forward(p.plan, p.x.t().contiguous().t()),
