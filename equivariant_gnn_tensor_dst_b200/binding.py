@@ -208,6 +208,14 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _raw_stream(stream, device):
+    """The stream handle as an integer (building a torch Stream object costs several microseconds)."""
+    import torch
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _need(t, dtype, name):
     import torch
     if t is None:
@@ -470,6 +478,12 @@ class Dropout:
                                  None if step is None else step.data_ptr())
         self._ref = ctypes.byref(self._spec)
 
+    def spec(self, device):
+        """The structure for a call on ``device``."""
+        if self.step is not None and self.step.device != device:
+            raise ValueError(f"step must be on {device}")
+        return self._ref
+
     @property
     def p(self):
         return self._spec.p
@@ -487,38 +501,39 @@ class Dropout:
         self._spec.offset = int(value) & (2 ** 64 - 1)
 
 
-def _node_rows(plan, device, *arrays):
-    """Rows N of node arrays ((tensor, name), the first one required), all [N, dim] in the plan's
-    type, on one device."""
-    N = None
-    for t, name in arrays:
-        if t is None:
-            if N is None:
-                raise ValueError(f"{name} is required")
-            continue
-        _need(t, plan.dtype, name)
-        if t.dim() != 2 or t.shape[1] != plan.dim:
-            raise ValueError(f"{name} must have {plan.dim} columns")
-        if N is None:
-            N = t.shape[0]
-        if t.shape[0] != N:
-            raise ValueError(f"{name} must have {N} rows")
-        if t.device != device:
-            raise ValueError(f"{name} must be on {device}")
-    return N
+def _node_bad(t, name, dtype, shape, device):
+    """Says what is wrong with an array that failed the one-line check."""
+    _need(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
+    raise ValueError(f"{name} must be on {device}")
 
 
-def _node_params(device, *arrays):
-    """Channel vectors: (tensor or None, length, name)."""
+def _node_ptrs(plan, x, name, rows, params):
+    """Checks node arrays (``rows``: (tensor or None, name), of x's shape, in the plan's type) and
+    channel vectors (``params``: (tensor or None, length, name), float32), all contiguous and on
+    x's device; returns their addresses (0 for None) in that order, x first."""
     import torch
-    for t, n, name in arrays:
+    dtype, shape, device = plan.dtype, x.shape, x.device
+    if not (x.is_cuda and x.dtype is dtype and x.is_contiguous() and len(shape) == 2 and shape[1] == plan.dim):
+        _need(x, dtype, name)
+        raise ValueError(f"{name} must be [rows, {plan.dim}], not {list(shape)}")
+    ptrs = [x.data_ptr()]
+    for t, what in rows:
         if t is None:
+            ptrs.append(0)
             continue
-        _need(t, torch.float32, name)
-        if t.numel() != n:
-            raise ValueError(f"{name} must have {n} values")
-        if t.device != device:
-            raise ValueError(f"{name} must be on {device}")
+        if not (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+            _node_bad(t, what, dtype, shape, device)
+        ptrs.append(t.data_ptr())
+    for t, n, what in params:
+        if t is None:
+            ptrs.append(0)
+            continue
+        if not (t.dtype is torch.float32 and t.numel() == n and t.device == device and t.is_contiguous()):
+            _node_bad(t, what, torch.float32, (n,), device)
+        ptrs.append(t.data_ptr())
+    return ptrs
 
 
 def _node_call(device, name, stream, *args):
@@ -527,26 +542,28 @@ def _node_call(device, name, stream, *args):
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
             return _node_call(device, name, stream, *args)
-    check(getattr(lib(), name)(*args, _stream(stream)), name)
+    status = getattr(_lib, name)(*args, _raw_stream(stream, device))
+    if status:
+        raise TPConvError(status, name)
 
 
 def _node_ws(plan, N, ws, device):
+    """(workspace kept alive, address, bytes)"""
     if ws is None:
-        return workspace(plan.workspace_bytes(N), device)
-    if not ws.is_cuda or ws.device != device:
-        raise ValueError(f"ws must be on {device}")
-    return ws
+        ws = workspace(plan.workspace_bytes(N), device)
+    elif ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous and on {device}")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def tpconv_norm_forward(plan, x, weight=None, bias=None, out=None, stream=None):
     """Irreps layer norm of node rows x [N, dim]; weight [channels], bias [biases] float32."""
     import torch
-    dev = x.device
     if out is None:
         out = torch.empty_like(x)
-    N = _node_rows(plan, dev, (x, "x"), (out, "out"))
-    _node_params(dev, (weight, plan.channels, "weight"), (bias, plan.biases, "bias"))
-    _node_call(dev, "tpconv_norm_forward", stream, plan.handle, N, _ptr(x), _ptr(weight), _ptr(bias), _ptr(out))
+    px, po, pw, pb = _node_ptrs(plan, x, "x", ((out, "out"),),
+                                ((weight, plan.channels, "weight"), (bias, plan.biases, "bias")))
+    _node_call(x.device, "tpconv_norm_forward", stream, plan.handle, x.shape[0], px, pw, pb, po)
     return out
 
 
@@ -554,19 +571,18 @@ def tpconv_norm_backward(plan, x, weight, grad_y, need_x=True, need_weight=True,
                          outputs=None, stream=None):
     """Returns (grad_x [N, dim], grad_weight [channels], grad_bias [biases])."""
     import torch
-    dev = x.device
+    dev, N = x.device, x.shape[0]
     if outputs is None:
         gx = torch.empty_like(x) if need_x else None
         gw = torch.empty(plan.channels, dtype=torch.float32, device=dev) if need_weight else None
         gb = torch.empty(plan.biases, dtype=torch.float32, device=dev) if need_bias else None
     else:
         gx, gw, gb = outputs
-    N = _node_rows(plan, dev, (x, "x"), (grad_y, "grad_y"), (gx, "grad_x"))
-    _node_params(dev, (weight, plan.channels, "weight"), (gw, plan.channels, "grad_weight"),
-                 (gb, plan.biases, "grad_bias"))
-    ws = _node_ws(plan, N, ws, dev)
-    _node_call(dev, "tpconv_norm_backward", stream, plan.handle, N, _ptr(x), _ptr(weight), _ptr(grad_y), _ptr(gx),
-               _ptr(gw), _ptr(gb), _ptr(ws), ws.numel() * ws.element_size())
+    px, pg, pgx, pw, pgw, pgb = _node_ptrs(
+        plan, x, "x", ((grad_y, "grad_y"), (gx, "grad_x")),
+        ((weight, plan.channels, "weight"), (gw, plan.channels, "grad_weight"), (gb, plan.biases, "grad_bias")))
+    ws, pws, nws = _node_ws(plan, N, ws, dev)
+    _node_call(dev, "tpconv_norm_backward", stream, plan.handle, N, px, pw, pg, pgx, pgw, pgb, pws, nws)
     return gx, gw, gb
 
 
@@ -574,54 +590,52 @@ def tpconv_norm_double_backward(plan, x, weight, grad_y, gg_x=None, gg_weight=No
                                 need_weight=True, need_grad_y=True, ws=None, outputs=None, stream=None):
     """Returns (grad_x [N, dim], grad_weight [channels], grad_grad_y [N, dim])."""
     import torch
-    dev = x.device
+    dev, N = x.device, x.shape[0]
     if outputs is None:
         gx = torch.empty_like(x) if need_x else None
         gw = torch.empty(plan.channels, dtype=torch.float32, device=dev) if need_weight else None
         gg = torch.empty_like(x) if need_grad_y else None
     else:
         gx, gw, gg = outputs
-    N = _node_rows(plan, dev, (x, "x"), (grad_y, "grad_y"), (gg_x, "gg_x"), (gx, "grad_x"), (gg, "grad_grad_y"))
-    _node_params(dev, (weight, plan.channels, "weight"), (gg_weight, plan.channels, "gg_weight"),
-                 (gg_bias, plan.biases, "gg_bias"), (gw, plan.channels, "grad_weight"))
-    ws = _node_ws(plan, N, ws, dev)
-    _node_call(dev, "tpconv_norm_double_backward", stream, plan.handle, N, _ptr(x), _ptr(weight), _ptr(grad_y),
-               _ptr(gg_x), _ptr(gg_weight), _ptr(gg_bias), _ptr(gx), _ptr(gw), _ptr(gg), _ptr(ws),
-               ws.numel() * ws.element_size())
+    px, pg, pp, pgx, pgg, pw, pt, ptb, pgw = _node_ptrs(
+        plan, x, "x", ((grad_y, "grad_y"), (gg_x, "gg_x"), (gx, "grad_x"), (gg, "grad_grad_y")),
+        ((weight, plan.channels, "weight"), (gg_weight, plan.channels, "gg_weight"), (gg_bias, plan.biases, "gg_bias"),
+         (gw, plan.channels, "grad_weight")))
+    ws, pws, nws = _node_ws(plan, N, ws, dev)
+    _node_call(dev, "tpconv_norm_double_backward", stream, plan.handle, N, px, pw, pg, pp, pt, ptb, pgx, pgw, pgg,
+               pws, nws)
     return gx, gw, gg
 
 
 def tpconv_dropout_forward(plan, x, dropout, residual=None, out=None, stream=None):
     """residual + dropout(x); ``dropout`` is a Dropout.  out may be x or residual (in place)."""
     import torch
-    dev = x.device
     if out is None:
         out = torch.empty_like(x)
-    N = _node_rows(plan, dev, (x, "x"), (residual, "residual"), (out, "out"))
-    _node_call(dev, "tpconv_dropout_forward", stream, plan.handle, N, _ptr(x), _ptr(residual), dropout._ref, _ptr(out))
+    px, pr, po = _node_ptrs(plan, x, "x", ((residual, "residual"), (out, "out")), ())
+    _node_call(x.device, "tpconv_dropout_forward", stream, plan.handle, x.shape[0], px, pr, dropout.spec(x.device), po)
     return out
 
 
 def tpconv_dropout_backward(plan, grad_out, dropout, out=None, stream=None):
     """grad_x of tpconv_dropout_forward (the residual's gradient is grad_out itself)."""
     import torch
-    dev = grad_out.device
     if out is None:
         out = torch.empty_like(grad_out)
-    N = _node_rows(plan, dev, (grad_out, "grad_out"), (out, "out"))
-    _node_call(dev, "tpconv_dropout_backward", stream, plan.handle, N, _ptr(grad_out), dropout._ref, _ptr(out))
+    pg, po = _node_ptrs(plan, grad_out, "grad_out", ((out, "out"),), ())
+    _node_call(grad_out.device, "tpconv_dropout_backward", stream, plan.handle, grad_out.shape[0], pg,
+               dropout.spec(grad_out.device), po)
     return out
 
 
 def tpconv_dropout_norm_forward(plan, x, dropout, residual=None, weight=None, bias=None, outputs=None, stream=None):
     """Returns (z, y): z = residual + dropout(x), y = norm(z)."""
     import torch
-    dev = x.device
     z, y = (torch.empty_like(x), torch.empty_like(x)) if outputs is None else outputs
-    N = _node_rows(plan, dev, (x, "x"), (z, "z"), (y, "y"), (residual, "residual"))
-    _node_params(dev, (weight, plan.channels, "weight"), (bias, plan.biases, "bias"))
-    _node_call(dev, "tpconv_dropout_norm_forward", stream, plan.handle, N, _ptr(x), _ptr(residual), dropout._ref,
-               _ptr(weight), _ptr(bias), _ptr(z), _ptr(y))
+    px, pr, pz, py, pw, pb = _node_ptrs(plan, x, "x", ((residual, "residual"), (z, "z"), (y, "y")),
+                                        ((weight, plan.channels, "weight"), (bias, plan.biases, "bias")))
+    _node_call(x.device, "tpconv_dropout_norm_forward", stream, plan.handle, x.shape[0], px, pr,
+               dropout.spec(x.device), pw, pb, pz, py)
     return z, y
 
 
@@ -629,7 +643,7 @@ def tpconv_dropout_norm_backward(plan, z, weight, grad_y, dropout, grad_z=None, 
                                  need_weight=True, need_bias=True, ws=None, outputs=None, stream=None):
     """Returns (grad_x, grad_residual, grad_weight, grad_bias) from the stored z."""
     import torch
-    dev = z.device
+    dev, N = z.device, z.shape[0]
     if outputs is None:
         gx = torch.empty_like(z) if need_x else None
         gr = torch.empty_like(z) if need_residual else None
@@ -637,14 +651,12 @@ def tpconv_dropout_norm_backward(plan, z, weight, grad_y, dropout, grad_z=None, 
         gb = torch.empty(plan.biases, dtype=torch.float32, device=dev) if need_bias else None
     else:
         gx, gr, gw, gb = outputs
-    N = _node_rows(plan, dev, (z, "z"), (grad_y, "grad_y"), (grad_z, "grad_z"), (gx, "grad_x"),
-                   (gr, "grad_residual"))
-    _node_params(dev, (weight, plan.channels, "weight"), (gw, plan.channels, "grad_weight"),
-                 (gb, plan.biases, "grad_bias"))
-    ws = _node_ws(plan, N, ws, dev)
-    _node_call(dev, "tpconv_dropout_norm_backward", stream, plan.handle, N, _ptr(z), _ptr(weight), _ptr(grad_y),
-               _ptr(grad_z), dropout._ref, _ptr(gx), _ptr(gr), _ptr(gw), _ptr(gb), _ptr(ws),
-               ws.numel() * ws.element_size())
+    pz, pg, pgz, pgx, pgr, pw, pgw, pgb = _node_ptrs(
+        plan, z, "z", ((grad_y, "grad_y"), (grad_z, "grad_z"), (gx, "grad_x"), (gr, "grad_residual")),
+        ((weight, plan.channels, "weight"), (gw, plan.channels, "grad_weight"), (gb, plan.biases, "grad_bias")))
+    ws, pws, nws = _node_ws(plan, N, ws, dev)
+    _node_call(dev, "tpconv_dropout_norm_backward", stream, plan.handle, N, pz, pw, pg, pgz, dropout.spec(dev), pgx,
+               pgr, pgw, pgb, pws, nws)
     return gx, gr, gw, gb
 
 

@@ -6,16 +6,18 @@
 // is read once, the statistics are sums over the lanes that hold a segment, and outputs are
 // written from the same registers; arithmetic is two float32 values an instruction (f32x2).
 //
-//  * k_fwd / k_bwd / k_dbl<WIDE = false>: a segment is held by a group of G lanes (a power of two,
-//    at most a warp), lane l holding the packs l, l + G, ... of V elements, J packs at most.  A CTA
-//    serves one block of the irreps and strides over rows; the blocks share the CTAs in proportion
-//    to their sizes, so that all of them walk through the rows at the same pace in one wave.
-//    A lane's columns are the same in every row: the sums over rows are per-lane registers until
-//    the rows are done, weights are expanded per element in shared memory once.
+//  * k_fwd / k_bwd / k_dbl: a segment is held by a group of G lanes (a power of two, up to the
+//    CTA), lane l holding the 16-byte packs l, l + G, ..., J packs at most.  A CTA serves one block
+//    of the irreps and strides over rows; every CTA makes the same number of steps, all of them in
+//    one wave.  A lane's columns are the same in every row: the sums over rows are per-lane
+//    registers until the rows are done, weights are expanded per element in shared memory once.
 //  * Rows are copied ahead with cp.async into a ring of shared memory slots that belong to the
 //    thread alone (no barriers, no registers held by loads in flight).
-//  * WIDE = true: the CTA is the group (segments beyond a warp's registers).
-//  * k_*_any: any width, the segment read again from cache for each sum.
+//  * EDGE = true: rows or blocks that start off a 16-byte boundary.  A CTA serves the rows n of one
+//    residue class (n mod R), in which a block has one offset from the boundary, so packs stay
+//    aligned and columns stay fixed; the first and last pack of a segment hold neighbours'
+//    elements, which are masked and not written.
+//  * k_*_any: segments beyond a CTA's registers, read again from cache for each sum.
 //
 // Sums over rows (weight and bias gradients) have no atomics: each CTA writes its partial sums to
 // the workspace and k_norm_reduce adds them in CTA order; a launch with one CTA per block writes
@@ -28,36 +30,32 @@ namespace tpc {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWide = 512;         // threads of a CTA whose only group is beyond 256 lanes
 constexpr int kSms = 148;
-constexpr int kWideMax = 512;      // threads of a WIDE CTA
 constexpr int kMaxSmem = 231 * 1000;  // dynamic shared memory of a CTA (the rest of 227 KB is static)
 constexpr int kAnyParts = 296;     // row ranges of the any-width kernels
 constexpr int kAnyFloats = 1 << 22;  // bound on their partial sums
 
-enum Kind { KIND_GROUP, KIND_WIDE, KIND_ANY };
-
 // Blocks served by one launch: CTAs [cta0[k], cta0[k + 1]) serve block blk[k].
 struct RowMap {
   int n;
+  int classes;                     // residue classes of rows (R), 1 unless EDGE
+  int direct;                      // one CTA per block: sums go to the gradients themselves
   int blk[MAX_BLOCKS];
   int cta0[MAX_BLOCKS + 1];
-  int lg[MAX_BLOCKS];              // log2 of the group's lanes (KIND_GROUP)
+  int lg[MAX_BLOCKS];              // log2 of the group's lanes
   long long part0[MAX_BLOCKS];     // first float of the block's partial sums
-  int direct;                      // one CTA per block: sums go to the gradients themselves
 };
 
-// The partial sums of one block: `parts` rows of weight sums (per channel, or per element of
-// which `comps` belong to a channel) followed by bias sums.
+// The partial sums of one block: `parts` rows of channel sums (weight, then bias of a 0e block).
 struct PartMap {
   int n;
   int blk[MAX_BLOCKS];
-  int parts[MAX_BLOCKS], comps[MAX_BLOCKS];
+  int parts[MAX_BLOCKS];
   long long part0[MAX_BLOCKS];
 };
 
-__host__ __device__ inline long long part_stride(const NodeBlock& B, int comps) {
-  return (long long)B.C * comps + (B.bias0 >= 0 ? B.C : 0);
-}
+__host__ __device__ inline long long part_stride(const NodeBlock& B) { return (long long)B.C * (B.bias0 >= 0 ? 2 : 1); }
 
 // ---- pairs of float32 ----
 
@@ -94,201 +92,262 @@ __device__ __forceinline__ float total(const f2 (&v)[P]) {
   return lo(s) + hi(s);
 }
 
-// Sums of K values over the CTA (any number of warps), to all its threads.
-template <int K>
-__device__ __forceinline__ void cta_sum(float (&v)[K]) {
-  __shared__ float part[32][K];
+// Sums of K values over W consecutive warps (each thread's own values), to all their threads, by
+// way of part[2][warps of the CTA][K] in shared memory: calls alternate between the two halves, and
+// none can be two calls ahead of another warp, so one barrier a call is enough.
+template <int K, class Sync>
+__device__ __forceinline__ void warps_sum(float (&v)[K], float* part, int& flip, int warp, int first, int W,
+                                          int warps, Sync sync) {
   group_sum(v, 32);
-  __syncthreads();  // the previous call's readers are done
+  float* half = part + flip * warps * K;
+  flip ^= 1;
   if ((threadIdx.x & 31) == 0)
 #pragma unroll
-    for (int k = 0; k < K; ++k) part[threadIdx.x >> 5][k] = v[k];
-  __syncthreads();
-  const int warps = blockDim.x >> 5;
+    for (int k = 0; k < K; ++k) half[warp * K + k] = v[k];
+  sync();
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = 0.f;
-  for (int w = 0; w < warps; ++w)
+  for (int w = first; w < first + W; ++w)
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += part[w][k];
+    for (int k = 0; k < K; ++k) v[k] += half[w * K + k];
 }
 
 // ---- segments in registers ----
 
 // A thread's place: its block, its lane of a group and the rows it serves.
-template <bool WIDE>
+template <int TH, bool EDGE>
 struct Place {
   NodeBlock B;
-  int k, G, lane, group;
-  int warp_group;                // the group of the warp's first lane
-  long long n, stride;
-  __device__ __forceinline__ Place(const NodeDesc& D, const RowMap& M) {
+  int k, lg, G, lane, group;
+  int shift;                     // EDGE: elements between the 16-byte boundary and the segment
+  uint32_t n, stride, warp_rows; // warp_rows: the thread's row minus that of the warp's first lane
+  uint32_t step;                 // elements between a lane's packs
+  float* part;                   // exchange between the warps of a group
+  mutable int flip;
+  __device__ __forceinline__ Place(const NodeDesc& D, const RowMap& M, int V, float* part_) : part(part_), flip(0) {
     k = 0;
     while (k + 1 < M.n && (int)blockIdx.x >= M.cta0[k + 1]) ++k;
     B = D.b[M.blk[k]];
-    const int lg = M.lg[k];
-    G = WIDE ? (int)blockDim.x : 1 << lg;
-    lane = WIDE ? (int)threadIdx.x : (int)threadIdx.x & (G - 1);
-    group = WIDE ? 0 : (int)threadIdx.x >> lg;
-    warp_group = WIDE ? 0 : ((int)threadIdx.x & ~31) >> lg;
-    const int rows = WIDE ? 1 : kThreads >> lg;
-    n = (long long)((int)blockIdx.x - M.cta0[k]) * rows + group;
-    stride = (long long)(M.cta0[k + 1] - M.cta0[k]) * rows;
+    lg = M.lg[k];
+    G = 1 << lg;
+    lane = (int)threadIdx.x & (G - 1);
+    group = (int)threadIdx.x >> lg;
+    step = G * V;
+    const uint32_t rows = TH >> lg, cta = blockIdx.x - M.cta0[k], ctas = M.cta0[k + 1] - M.cta0[k];
+    const uint32_t R = EDGE ? M.classes : 1, cls = EDGE ? cta % R : 0;
+    n = R * (cta / R * rows + group) + cls;
+    stride = ctas * rows;
+    warp_rows = G < 32 ? R * (((int)threadIdx.x & 31) >> lg) : 0;
+    shift = EDGE ? (int)(((long long)cls * D.dim + B.off) % V) : 0;
   }
   // whether any group of the warp has a row left (groups share shuffles)
-  __device__ __forceinline__ bool more(long long row, long long N) const { return row - (group - warp_group) < N; }
+  __device__ __forceinline__ bool more(uint32_t row, uint32_t N) const { return row - warp_rows < N; }
+  __device__ __forceinline__ void sync() const {
+    if (G <= 32) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(G) : "memory");
+  }
   template <int K>
   __device__ __forceinline__ void sum(float (&v)[K]) const {
-    if (WIDE) cta_sum(v);
-    else group_sum(v, G);
+    if (G <= 32) {
+      group_sum(v, G);
+    } else {
+      const int warp = (int)threadIdx.x >> 5, W = G >> 5;
+      warps_sum(v, part, flip, warp, warp & ~(W - 1), W, TH / 32, [&] { sync(); });
+    }
   }
-  __device__ __forceinline__ void sync() const {
-    if (WIDE) __syncthreads();
-    else __syncwarp();
-  }
+  // element of a lane's pack j (negative or >= S: not in the segment)
+  template <int V>
+  __device__ __forceinline__ int elem(int j) const { return (j * G + lane) * V - shift; }
 };
-
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t to, const void* from, int bytes) {
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(BYTES), "r"(bytes) : "memory");
-}
 
 // Slots of the copy ring: enough that a CTA has 16 KB or more on the way (as measured, more gains
 // nothing), two at least.
-__host__ __device__ constexpr int ring_slots(int esize, int elems, int arrays) {
-  const int bytes = arrays * elems * esize * kThreads;
-  return bytes >= 16384 ? 2 : bytes >= 8192 ? 3 : 4;
+__host__ __device__ constexpr int ring_slots(int pack_bytes) {
+  return pack_bytes * kThreads >= 16384 ? 2 : pack_bytes * kThreads >= 8192 ? 3 : 4;
 }
 
-// A thread's own packs of A arrays, copied ahead row by row.  Lanes beyond the segment and rows
-// beyond the last one read zeros (a copy of no bytes, from an address inside the array).  Packs
-// narrower than cp.async's four bytes are loaded when they are wanted.
-template <class T, int V, int J, int A>
+// A thread's own packs of A arrays, copied ahead row by row.  Packs beyond the segment hold zeros
+// from the start; slots of rows beyond the last one hold anything (such rows are computed, by
+// groups that share a warp with others, but neither stored nor summed).
+template <class T, int J, int A, int TH, bool EDGE>
 struct Ring {
-  static constexpr int kBytes = V * (int)sizeof(T), kSlots = ring_slots(sizeof(T), V * J, A);
-  static constexpr bool kAsync = kBytes >= 4;
-  const T* base[A];
-  char* mine;                // this thread's pack 0 of slot 0
-  int slot_bytes, pack_bytes;
-  int S, step, first;        // elements between packs, first element
-  long long dim, N, stride, ahead;
-  int fill, read;
+  static constexpr int V = 16 / sizeof(T), kSlots = ring_slots(16 * A * J);
+  static constexpr int kPack = 16 * TH, kSlot = A * J * kPack, kBytes = kSlots * kSlot;
+  const char* p[A];          // this lane's pack 0 in the row `ahead`; NULL: no such array
+  uint32_t mine, fill, read; // shared addresses: slot 0, next slot to fill, current slot
+  uint32_t ahead, N, stride;
+  uint32_t inside;           // bit j: pack j has elements of the segment
+  long long row_step, pack_step;
+  long long left;            // EDGE: bytes from p[] to the end of the arrays
 
-  __device__ __forceinline__ void start(char* smem, const NodeDesc& D, const NodeBlock& B, int lane, int G,
-                                        long long n, long long stride_, long long N_) {
-    pack_bytes = kBytes * (int)blockDim.x;
-    slot_bytes = A * J * pack_bytes;
-    mine = smem + kBytes * threadIdx.x;
-    S = B.S;
-    first = lane * V;
-    step = G * V;
-    dim = D.dim;
+  __device__ __forceinline__ void start(char* smem, const NodeDesc& D, const Place<TH, EDGE>& at, uint32_t N_,
+                                        const void* const (&arrays)[A]) {
+    mine = fill = read = (uint32_t)__cvta_generic_to_shared(smem) + 16 * threadIdx.x;
+    ahead = at.n;
     N = N_;
-    stride = stride_;
-    ahead = n;
-    fill = read = 0;
-    if constexpr (kAsync) {
+    stride = at.stride;
+    const long long first = (long long)ahead * D.dim + at.B.off + at.template elem<V>(0);
+    row_step = (long long)stride * D.dim * (int)sizeof(T);
+    pack_step = (long long)at.step * (int)sizeof(T);
+    left = ((long long)N * D.dim - first) * (int)sizeof(T);
 #pragma unroll
-      for (int i = 0; i < kSlots - 1; ++i) issue();
+    for (int a = 0; a < A; ++a) p[a] = arrays[a] ? (const char*)arrays[a] + first * (int)sizeof(T) : nullptr;
+    inside = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      if (at.template elem<V>(j) < at.B.S) {
+        inside |= 1u << j;
+      } else {
+#pragma unroll
+        for (int i = 0; i < kSlots * A; ++i)
+          *reinterpret_cast<uint4*>(smem + 16 * threadIdx.x + (i * J + j) * kPack) = make_uint4(0, 0, 0, 0);
+      }
     }
+#pragma unroll
+    for (int i = 0; i < kSlots - 1; ++i) issue();
   }
   // copies of the row `ahead` into the next slot
   __device__ __forceinline__ void issue() {
-    const bool ok = ahead < N;
-    const long long row = (ok ? ahead : N - 1) * dim;
-    const uint32_t to = (uint32_t)__cvta_generic_to_shared(mine + fill * slot_bytes);
+    if (ahead < N) {
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int s = first + j * step;
-      const bool in = s < S;
+      for (int a = 0; a < A; ++a) {
+        if (!p[a]) continue;
 #pragma unroll
-      for (int a = 0; a < A; ++a)
-        if (base[a])
-          copy_async<kBytes>(to + (a * J + j) * pack_bytes, base[a] + row + (in ? s : 0), ok && in ? kBytes : 0);
+        for (int j = 0; j < J; ++j) {
+          if (!(inside >> j & 1)) continue;
+          const char* from = p[a] + j * pack_step;
+          int bytes = 16;  // the arrays' last pack may be cut short
+          if (EDGE && left - j * pack_step < 16) bytes = (int)(left - j * pack_step);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(fill + (a * J + j) * kPack), "l"(from),
+                       "r"(bytes)
+                       : "memory");
+        }
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     ahead += stride;
-    fill = fill + 1 == kSlots ? 0 : fill + 1;
+    left -= row_step;
+#pragma unroll
+    for (int a = 0; a < A; ++a)
+      if (p[a]) p[a] += row_step;
+    fill = fill == mine + (kSlots - 1) * kSlot ? mine : fill + kSlot;
   }
   // makes the next row readable and starts the copies of a later one
   __device__ __forceinline__ void next() {
-    if constexpr (kAsync) {
-      issue();
-      asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
-    }
+    issue();
+    asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
   }
-  // pairs of array a of the current row
-  __device__ __forceinline__ void get(int a, f2 (&v)[V * J / 2]) const {
-    Pack<T, V> p[J];
+  // pairs of array a of the current row; EDGE: `valid` marks the elements of the segment
+  __device__ __forceinline__ void get(int a, f2 (&v)[V * J / 2], uint32_t valid) const {
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      if constexpr (kAsync) {
-        p[j] = *reinterpret_cast<const Pack<T, V>*>(mine + read * slot_bytes + (a * J + j) * pack_bytes);
-      } else {
-        const int s = first + j * step;
+      uint32_t w[4];
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "r"(read + (a * J + j) * kPack)
+                   : "memory");
 #pragma unroll
-        for (int i = 0; i < V; ++i) p[j].v[i] = from_f32<T>(0.f);
-        if (ahead < N && s < S) p[j] = *reinterpret_cast<const Pack<T, V>*>(base[a] + ahead * dim + s);
+      for (int i = 0; i < V; i += 2) {
+        float x, y;
+        if constexpr (sizeof(T) == 4) {
+          x = __uint_as_float(w[i]);
+          y = __uint_as_float(w[i + 1]);
+        } else {
+          unpack<T>(w[i / 2], x, y);
+        }
+        if (EDGE) {
+          x = valid >> (j * V + i) & 1 ? x : 0.f;
+          y = valid >> (j * V + i + 1) & 1 ? y : 0.f;
+        }
+        v[(j * V + i) / 2] = pack2(x, y);
       }
     }
+  }
+  __device__ __forceinline__ void done() { read = read == mine + (kSlots - 1) * kSlot ? mine : read + kSlot; }
+  __device__ __forceinline__ void finish() const { asm volatile("cp.async.wait_all;" ::: "memory"); }
+};
+
+// A thread's packs of an output, row by row.
+template <class T, int J, int TH, bool EDGE>
+struct Out {
+  static constexpr int V = 16 / sizeof(T);
+  char* p;                   // this lane's pack 0 in the current row; NULL: not wanted
+  long long row_step, pack_step;
+  __device__ __forceinline__ Out(void* array, const NodeDesc& D, const Place<TH, EDGE>& at) {
+    const long long first = (long long)at.n * D.dim + at.B.off + at.template elem<V>(0);
+    p = array ? (char*)array + first * (int)sizeof(T) : nullptr;
+    row_step = (long long)at.stride * D.dim * (int)sizeof(T);
+    pack_step = (long long)at.step * (int)sizeof(T);
+  }
+  __device__ __forceinline__ explicit operator bool() const { return p != nullptr; }
+  __device__ __forceinline__ void put(const f2 (&v)[V * J / 2], uint32_t valid) const {
 #pragma unroll
-    for (int e = 0; e < V * J; e += 2)
-      v[e / 2] = pack2(to_f32(p[e / V].v[e % V]), to_f32(p[(e + 1) / V].v[(e + 1) % V]));
+    for (int j = 0; j < J; ++j) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        const f2 q = v[(j * V + i) / 2];
+        if constexpr (sizeof(T) == 4) {
+          w[i] = (uint32_t)q;
+          w[i + 1] = (uint32_t)(q >> 32);
+        } else {
+          w[i / 2] = pack<T>(lo(q), hi(q));
+        }
+      }
+      const uint32_t all = (1u << V) - 1, bits = valid >> (j * V) & all;
+      if (EDGE ? bits == all : bits != 0) {
+        *reinterpret_cast<uint4*>(p + j * pack_step) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else if (EDGE && bits) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (bits >> i & 1) {
+            if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(p + j * pack_step)[i] = w[i];
+            else reinterpret_cast<uint16_t*>(p + j * pack_step)[i] = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
+          }
+      }
+    }
   }
-  __device__ __forceinline__ void done() {
-    if constexpr (kAsync) read = read + 1 == kSlots ? 0 : read + 1;
-    else ahead += stride;
-  }
-  __device__ __forceinline__ void finish() const {
-    if constexpr (kAsync) asm volatile("cp.async.wait_all;" ::: "memory");
+  __device__ __forceinline__ void next() {
+    if (p) p += row_step;
   }
 };
 
-template <class T, int V, int J>
-__device__ __forceinline__ void store(T* row, const f2 (&v)[V * J / 2], int lane, int G, int S, bool ok) {
+// Bits of the lane's elements that belong to the segment, lowest first.
+template <int V, int J, class P>
+__device__ __forceinline__ uint32_t valid_bits(const P& at) {
+  uint32_t bits = 0;
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int s = (j * G + lane) * V;
-    if (!ok || s >= S) continue;
-    Pack<T, V> p;
+  for (int j = 0; j < J; ++j)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = j * V + i;
-      p.v[i] = from_f32<T>(e % 2 ? hi(v[e / 2]) : lo(v[e / 2]));
+      const int s = at.template elem<V>(j) + i;
+      if (s >= 0 && s < at.B.S) bits |= 1u << (j * V + i);
     }
-    *reinterpret_cast<Pack<T, V>*>(row + s) = p;
+  return bits;
+}
+
+// A channel vector expanded per element in shared memory, element s at [shift + s] of n (`missing`
+// where there is no vector, zeros outside the segment).
+__device__ __forceinline__ void expand(float* to, int n, const float* vec, const Channels& ch, int S, int shift,
+                                       float missing) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int s = i - shift;
+    to[i] = s < 0 || s >= S ? 0.f : vec ? vec[ch.of(s)] : missing;
   }
 }
 
-// A channel vector expanded per element in shared memory (`missing` where there is none).
-__device__ __forceinline__ void expand(float* to, const float* vec, const Channels& ch, int S, float missing) {
-  for (int s = threadIdx.x; s < S; s += blockDim.x) to[s] = vec ? vec[ch.of(s)] : missing;
-}
-
-// Pairs of an expanded vector at a lane's elements (anything beyond the segment).
-template <int V, int J>
-__device__ __forceinline__ void lookup(f2 (&w)[V * J / 2], const float* vec, int lane, int G, int S) {
+// Pairs of an expanded vector at a lane's elements.
+template <int V, int J, class P>
+__device__ __forceinline__ void lookup(f2 (&w)[V * J / 2], const float* vec, const P& at) {
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    int s = (j * G + lane) * V;
-    s = s < S ? s : 0;
-    if constexpr (V % 4 == 0) {
+  for (int j = 0; j < J; ++j)
 #pragma unroll
-      for (int i = 0; i < V; i += 4) {
-        const float4 q = *reinterpret_cast<const float4*>(vec + s + i);
-        w[(j * V + i) / 2] = pack2(q.x, q.y);
-        w[(j * V + i) / 2 + 1] = pack2(q.z, q.w);
-      }
-    } else if constexpr (V == 2) {
-      const float2 q = *reinterpret_cast<const float2*>(vec + s);
-      w[j] = pack2(q.x, q.y);
-    } else {
-      const float q = vec[s];
-      w[j / 2] = j % 2 ? pack2(lo(w[j / 2]), q) : pack2(q, 0.f);
+    for (int i = 0; i < V; i += 4) {
+      const int s = (j * at.G + at.lane) * V + i;
+      const float4 q = *reinterpret_cast<const float4*>(vec + s);
+      w[(j * V + i) / 2] = pack2(q.x, q.y);
+      w[(j * V + i) / 2 + 1] = pack2(q.z, q.w);
     }
-  }
 }
 
 // Keep bits of a segment's channel groups (four channels each, one byte per group) in shared
@@ -298,15 +357,16 @@ struct Mask {
   unsigned char* m;   // this group's bytes
   bool quads;         // packs lie inside one component and start on a multiple of four channels
   uint64_t off;
-  __device__ __forceinline__ Mask(unsigned char* all, int slot, const NodeDesc& D, const NodeBlock& B,
-                                  const Drop& drop) {
-    m = all + slot * ((B.C + 3) / 4);
-    quads = V % 4 == 0 && (B.d == 1 || (!D.mul_ir && B.C % V == 0));
+  template <class P>
+  __device__ __forceinline__ Mask(unsigned char* all, const P& at, const NodeDesc& D, const Drop& drop) {
+    m = all + at.group * ((at.B.C + 3) / 4);
+    quads = at.shift == 0 && (at.B.d == 1 || (!D.mul_ir && at.B.C % V == 0));
     off = drop.mode == 1 ? drop_offset(drop) : 0;
   }
   // keep bits of a lane's elements in a row, lowest first
   template <class P>
-  __device__ __forceinline__ uint32_t bits(const Drop& drop, const P& at, const Channels& ch, uint32_t row) {
+  __device__ __forceinline__ uint32_t bits(const Drop& drop, const P& at, const Channels& ch, uint32_t row,
+                                           uint32_t valid) {
     if (drop.mode != 1) return drop.mode == 0 ? ~0u : 0u;
     at.sync();  // the previous row's readers are done
     const int groups = (at.B.C + 3) / 4;
@@ -320,21 +380,21 @@ struct Mask {
     if (quads) {
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        const int s = (j * at.G + at.lane) * V;
-        const int c = s < at.B.S ? ch.of(s) >> 2 : 0;
+        const int c = valid >> (j * V) & 1 ? ch.of(at.template elem<V>(j)) >> 2 : 0;
+        // a cut last pack reads bytes of groups that are not there: its bits are not used
 #pragma unroll
         for (int i = 0; i < V / 4; ++i) keep |= (uint32_t)m[c + i] << (j * V + 4 * i);
       }
     } else {
 #pragma unroll 1
       for (int j = 0; j < J; ++j) {
-        const int s = (j * at.G + at.lane) * V;
-        if (s >= at.B.S) break;
+        const int s = at.template elem<V>(j);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int c = ch.of(s + i);
-          keep |= ((uint32_t)m[c >> 2] >> (c & 3) & 1u) << (j * V + i);
-        }
+        for (int i = 0; i < V; ++i)
+          if (valid >> (j * V + i) & 1) {
+            const int c = ch.of(s + i);
+            keep |= ((uint32_t)m[c >> 2] >> (c & 3) & 1u) << (j * V + i);
+          }
       }
     }
     return keep;
@@ -353,195 +413,190 @@ __device__ __forceinline__ void apply_mask(f2 (&v)[P], uint32_t keep, float scal
 }
 
 // v + m at the lane's elements inside the segment (the others hold zeros)
-template <int V, int J>
-__device__ __forceinline__ void shift(f2 (&v)[V * J / 2], float m, int lane, int G, int S) {
+template <int V, int J, bool EDGE>
+__device__ __forceinline__ void shift_by(f2 (&v)[V * J / 2], float m, uint32_t valid) {
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    const float t = (j * G + lane) * V < S ? m : 0.f;
-    if constexpr (V == 1) {
-      v[j / 2] = j % 2 ? pack2(lo(v[j / 2]), hi(v[j / 2]) + t) : pack2(lo(v[j / 2]) + t, hi(v[j / 2]));
-    } else {
+    if constexpr (EDGE) {
 #pragma unroll
-      for (int i = 0; i < V; i += 2) v[(j * V + i) / 2] = add2(v[(j * V + i) / 2], both(t));
+      for (int i = 0; i < V; i += 2)
+        v[(j * V + i) / 2] = add2(v[(j * V + i) / 2], pack2(valid >> (j * V + i) & 1 ? m : 0.f,
+                                                            valid >> (j * V + i + 1) & 1 ? m : 0.f));
+    } else {
+      const f2 t = both(valid >> (j * V) & 1 ? m : 0.f);
+#pragma unroll
+      for (int i = 0; i < V; i += 2) v[(j * V + i) / 2] = add2(v[(j * V + i) / 2], t);
     }
   }
 }
 
-// Shared memory of a CTA: the ring (after the rows: the sums over them), then vectors expanded per
-// element, then keep bits.
-__host__ __device__ constexpr int rows_bytes(int esize, int V, int elems, int arrays, bool sums, int threads) {
-  const int ring = V * esize < 4 ? 0 : ring_slots(esize, elems, arrays) * arrays * elems * esize * threads;
-  const int acc = sums ? threads * elems * 4 : 0;
+// Shared memory of a CTA: the ring (after the rows: the sums over them), vectors expanded per
+// element, the exchange between warps, keep bits.
+__host__ __device__ constexpr int rows_bytes(int elems, int arrays, int packs, bool sums, int threads) {
+  const int ring = ring_slots(16 * arrays * packs) * 16 * arrays * packs * threads, acc = sums ? threads * elems * 4 : 0;
   return ring > acc ? ring : acc;
 }
-__host__ __device__ constexpr int vector_bytes(int S) { return (S + 3) / 4 * 16; }
-constexpr int mask_bytes(int elems, int threads) { return threads * elems / 4 + threads + 4; }
+// a vector's elements as far as any lane reads them
+__host__ __device__ constexpr int vector_bytes(int elems, int lg) { return (elems << lg) * 4; }
+constexpr int kPartBytes = 2 * (kWide / 32) * 5 * 4;  // up to five sums at a time
+constexpr int mask_bytes(int elems, int threads) { return threads * elems / 4 + threads + 8; }
 
 extern __shared__ __align__(16) char g_smem[];
 
+#define TPC_NODE_KERNEL(TH, MIN) __global__ void __launch_bounds__(TH, (TH) == kThreads ? (MIN) : 1)
+
 // Dropout (DROP) and norm (NORM) of x, either or both; with DROP the sum with the residual is z.
-template <class T, int V, int J, bool WIDE, bool DROP, bool NORM>
-__global__ void __launch_bounds__(WIDE ? kWideMax : kThreads, WIDE ? 1 : 2)
+template <class T, int J, int TH, bool EDGE, bool DROP, bool NORM>
+TPC_NODE_KERNEL(TH, 2)
     k_fwd(const __grid_constant__ NodeDesc D, const __grid_constant__ RowMap M, const __grid_constant__ Drop drop,
-          const __grid_constant__ NormArgs A, const long long N) {
-  constexpr int P = V * J / 2, R = DROP ? 2 : 1;
-  const Place<WIDE> at(D, M);
+          const __grid_constant__ NormArgs A, const uint32_t N) {
+  constexpr int V = 16 / sizeof(T), E = V * J, P = E / 2, R = DROP ? 2 : 1;
+  float* part = reinterpret_cast<float*>(g_smem + rows_bytes(E, R, J, false, TH));
+  const Place<TH, EDGE> at(D, M, V, part);
   const NodeBlock& B = at.B;
-  const int S = B.S, G = at.G, lane = at.lane;
   const Channels ch(D, B);
   const bool centred = NORM && B.bias0 >= 0;
-  const float inv = 1.f / (float)S;
-  float* sw = reinterpret_cast<float*>(g_smem + rows_bytes(sizeof(T), V, V * J, R, false, blockDim.x));
-  float* sb = sw + (S + 3) / 4 * 4;
-  unsigned char* bytes = reinterpret_cast<unsigned char*>(sw + (NORM ? 2 * ((S + 3) / 4 * 4) : 0));
-  Ring<T, V, J, R> ring;
-  ring.base[0] = (const T*)A.x + B.off;
-  if constexpr (DROP) ring.base[R - 1] = A.residual ? (const T*)A.residual + B.off : nullptr;
-  ring.start(g_smem, D, B, lane, G, at.n, at.stride, N);
+  const float inv = 1.f / (float)B.S;
+  float* sw = reinterpret_cast<float*>(reinterpret_cast<char*>(part) + kPartBytes);
+  float* sb = sw + (E << at.lg);
+  Ring<T, J, R, TH, EDGE> ring;
+  if constexpr (DROP) ring.start(g_smem, D, at, N, {A.x, A.residual});
+  else ring.start(g_smem, D, at, N, {A.x});
   if constexpr (NORM) {
-    expand(sw, A.weight ? A.weight + B.chan0 : nullptr, ch, S, 1.f);
-    expand(sb, centred && A.bias ? A.bias + B.bias0 : nullptr, ch, S, 0.f);
+    expand(sw, E << at.lg, A.weight ? A.weight + B.chan0 : nullptr, ch, B.S, at.shift, 1.f);
+    expand(sb, E << at.lg, centred && A.bias ? A.bias + B.bias0 : nullptr, ch, B.S, at.shift, 0.f);
     __syncthreads();
   }
-  Mask<V, J> mask(bytes, at.group, D, B, drop);
-  const bool res = DROP && A.residual;
-  T *y = NORM ? (T*)A.y + B.off : nullptr, *z = DROP ? (T*)A.z + B.off : nullptr;
-  for (long long n = at.n; at.more(n, N); n += at.stride) {
+  Mask<V, J> mask(reinterpret_cast<unsigned char*>(NORM ? sb + (E << at.lg) : sw), at, D, drop);
+  const uint32_t valid = valid_bits<V, J>(at);
+  Out<T, J, TH, EDGE> y(NORM ? A.y : nullptr, D, at), z(DROP ? A.z : nullptr, D, at);
+  for (uint32_t n = at.n; at.more(n, N); n += at.stride) {
     const bool ok = n < N;
     ring.next();
     f2 v[P];
-    ring.get(0, v);
+    ring.get(0, v, valid);
     if constexpr (DROP) {
-      apply_mask(v, mask.bits(drop, at, ch, (uint32_t)n), drop.scale);
-      if (res) {
+      apply_mask(v, mask.bits(drop, at, ch, n, valid), drop.scale);
+      if (A.residual) {
         f2 r[P];
-        ring.get(R - 1, r);
+        ring.get(R - 1, r, valid);
 #pragma unroll
         for (int p = 0; p < P; ++p) v[p] = add2(v[p], r[p]);
       }
-      store<T, V, J>(z + n * D.dim, v, lane, G, S, ok);
+      if (ok) z.put(v, valid);
+      z.next();
     }
     if constexpr (NORM) {
       if (centred) {
         float mu[1] = {total(v)};
         at.sum(mu);
-        shift<V, J>(v, -mu[0] * inv, lane, G, S);
+        shift_by<V, J, EDGE>(v, -mu[0] * inv, valid);
       }
-      f2 q2[P];
+      f2 q2 = mul2(v[0], v[0]);
 #pragma unroll
-      for (int p = 0; p < P; ++p) q2[p] = mul2(v[p], v[p]);
-      float q[1] = {total(q2)};
+      for (int p = 1; p < P; ++p) q2 = fma2(v[p], v[p], q2);
+      float q[1] = {lo(q2) + hi(q2)};
       at.sum(q);
       const f2 r = both(__frsqrt_rn(q[0] * inv + D.eps));
       f2 w[P], b[P];
-      lookup<V, J>(w, sw, lane, G, S);
-      lookup<V, J>(b, sb, lane, G, S);
+      lookup<V, J>(w, sw, at);
+      lookup<V, J>(b, sb, at);
 #pragma unroll
       for (int p = 0; p < P; ++p) v[p] = fma2(mul2(v[p], r), w[p], b[p]);
-      store<T, V, J>(y + n * D.dim, v, lane, G, S, ok);
+      if (ok) y.put(v, valid);
+      y.next();
     }
     ring.done();
   }
   ring.finish();
 }
 
-// Adds the lanes' sums over rows of a CTA and writes them per channel (per element if WIDE).
-template <int V, int J, bool WIDE>
+// Adds the lanes' sums over rows of a CTA and writes them per channel.
+template <int V, int J, int TH, bool EDGE>
 __device__ __forceinline__ void write_sums(const f2 (&sums)[V * J / 2], float* smem, float* out,
-                                           const Place<WIDE>& at, const Channels& ch) {
+                                           const Place<TH, EDGE>& at, const Channels& ch) {
   constexpr int E = V * J;
   const int S = at.B.S, G = at.G;
-  if constexpr (WIDE) {
+  float acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = e % 2 ? hi(sums[e / 2]) : lo(sums[e / 2]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (G <= o) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], o);
+    }
+  __syncthreads();  // the ring, or earlier sums, have been read
+  // copies of the segment: one per warp, or per group of several warps
+  const int copies = G <= 32 ? TH / 32 : TH / G, copy = G <= 32 ? (int)threadIdx.x >> 5 : at.group;
+  if (G > 32 || ((int)threadIdx.x & 31) < G) {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int s = (e / V * G + at.lane) * V + e % V;
-      if (s < S) out[s] = e % 2 ? hi(sums[e / 2]) : lo(sums[e / 2]);
+      const int s = at.template elem<V>(e / V) + e % V;
+      if (s >= 0 && s < S) smem[copy * S + s] = acc[e];
     }
-  } else {
-    float acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = e % 2 ? hi(sums[e / 2]) : lo(sums[e / 2]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      if (G <= o) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], o);
-      }
-    __syncthreads();  // the ring, or earlier sums, have been read
-    const int warp = threadIdx.x >> 5;
-    if (((int)threadIdx.x & 31) < G) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int s = (e / V * G + at.lane) * V + e % V;
-        if (s < S) smem[warp * S + s] = acc[e];
-      }
-    }
-    __syncthreads();
-    for (int c = threadIdx.x; c < at.B.C; c += kThreads) {
-      float v = 0.f;
-      for (int m = 0; m < at.B.d; ++m)
-#pragma unroll
-        for (int k = 0; k < kThreads / 32; ++k) v += smem[k * S + ch.at(c, m)];
-      out[c] = v;
-    }
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < at.B.C; c += TH) {
+    float v = 0.f;
+    for (int m = 0; m < at.B.d; ++m)
+      for (int k = 0; k < copies; ++k) v += smem[k * S + ch.at(c, m)];
+    out[c] = v;
   }
 }
 
 // Where a CTA's weight (or bias) sums go.
-__device__ __forceinline__ float* sums_out(const RowMap& M, const NodeBlock& B, int k, int comps, float* partial,
-                                           float* grad, int first, bool bias) {
+__device__ __forceinline__ float* sums_out(const RowMap& M, const NodeBlock& B, int k, float* partial, float* grad,
+                                           int first, bool bias) {
   if (M.direct) return grad ? grad + first : nullptr;
   if (!partial) return nullptr;
-  return partial + M.part0[k] + ((int)blockIdx.x - M.cta0[k]) * part_stride(B, comps) +
-         (bias ? (long long)B.C * comps : 0);
+  return partial + M.part0[k] + ((int)blockIdx.x - M.cta0[k]) * part_stride(B) + (bias ? B.C : 0);
 }
 
-template <class T, int V, int J, bool WIDE, bool DROP>
-__global__ void __launch_bounds__(WIDE ? kWideMax : kThreads, WIDE ? 1 : 2)
+template <class T, int J, int TH, bool EDGE, bool DROP>
+TPC_NODE_KERNEL(TH, 2)
     k_bwd(const __grid_constant__ NodeDesc D, const __grid_constant__ RowMap M, const __grid_constant__ Drop drop,
-          const __grid_constant__ NormArgs A, const long long N) {
-  constexpr int P = V * J / 2, R = DROP ? 3 : 2;
-  const Place<WIDE> at(D, M);
+          const __grid_constant__ NormArgs A, const uint32_t N) {
+  constexpr int V = 16 / sizeof(T), E = V * J, P = E / 2, R = DROP ? 3 : 2;
+  float* part = reinterpret_cast<float*>(g_smem + rows_bytes(E, R, J, true, TH));
+  const Place<TH, EDGE> at(D, M, V, part);
   const NodeBlock& B = at.B;
-  const int S = B.S, G = at.G, lane = at.lane;
   const Channels ch(D, B);
   const bool centred = B.bias0 >= 0;
-  const float inv = 1.f / (float)S;
-  float* ws = reinterpret_cast<float*>(g_smem + rows_bytes(sizeof(T), V, V * J, R, !WIDE, blockDim.x));
-  unsigned char* bytes = reinterpret_cast<unsigned char*>(ws + (S + 3) / 4 * 4);
-  Ring<T, V, J, R> ring;
-  ring.base[0] = (const T*)A.x + B.off;
-  ring.base[1] = (const T*)A.grad_y + B.off;
-  if constexpr (DROP) ring.base[R - 1] = A.grad_z ? (const T*)A.grad_z + B.off : nullptr;
-  ring.start(g_smem, D, B, lane, G, at.n, at.stride, N);
-  expand(ws, A.weight ? A.weight + B.chan0 : nullptr, ch, S, 1.f);
+  const float inv = 1.f / (float)B.S;
+  float* ws = reinterpret_cast<float*>(reinterpret_cast<char*>(part) + kPartBytes);
+  Ring<T, J, R, TH, EDGE> ring;
+  if constexpr (DROP) ring.start(g_smem, D, at, N, {A.x, A.grad_y, A.grad_z});
+  else ring.start(g_smem, D, at, N, {A.x, A.grad_y});
+  expand(ws, E << at.lg, A.weight ? A.weight + B.chan0 : nullptr, ch, B.S, at.shift, 1.f);
   __syncthreads();
-  Mask<V, J> mask(bytes, at.group, D, B, drop);
+  Mask<V, J> mask(reinterpret_cast<unsigned char*>(ws + (E << at.lg)), at, D, drop);
+  const uint32_t valid = valid_bits<V, J>(at);
   f2 sw[P], sb[P];
 #pragma unroll
   for (int p = 0; p < P; ++p) sw[p] = sb[p] = 0;
-  const bool gz = DROP && A.grad_z;
-  T *gx = A.grad_x ? (T*)A.grad_x + B.off : nullptr, *gr = DROP && A.grad_residual ? (T*)A.grad_residual + B.off : nullptr;
-  for (long long n = at.n; at.more(n, N); n += at.stride) {
+  Out<T, J, TH, EDGE> gx(A.grad_x, D, at), gr(DROP ? A.grad_residual : nullptr, D, at);
+  for (uint32_t n = at.n; at.more(n, N); n += at.stride) {
     const bool ok = n < N;
     ring.next();
     f2 u[P], a[P];
-    ring.get(0, u);
+    ring.get(0, u, valid);
     {
       f2 w[P];
-      ring.get(1, a);
-      lookup<V, J>(w, ws, lane, G, S);
+      ring.get(1, a, valid);
+      lookup<V, J>(w, ws, at);
+      if (centred && ok) {
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        sb[p] = add2(sb[p], a[p]);
-        a[p] = mul2(a[p], w[p]);
+        for (int p = 0; p < P; ++p) sb[p] = add2(sb[p], a[p]);
       }
+#pragma unroll
+      for (int p = 0; p < P; ++p) a[p] = mul2(a[p], w[p]);
     }
     if (centred) {
       float m[2] = {total(u), total(a)};
       at.sum(m);
-      shift<V, J>(u, -m[0] * inv, lane, G, S);
-      shift<V, J>(a, -m[1] * inv, lane, G, S);
+      shift_by<V, J, EDGE>(u, -m[0] * inv, valid);
+      shift_by<V, J, EDGE>(a, -m[1] * inv, valid);
     }
     f2 q0 = mul2(u[0], u[0]), q1 = mul2(u[0], a[0]);
 #pragma unroll
@@ -554,79 +609,78 @@ __global__ void __launch_bounds__(WIDE ? kWideMax : kThreads, WIDE ? 1 : 2)
     const float r = __frsqrt_rn(q[0] * inv + D.eps);
     {
       f2 g[P];
-      ring.get(1, g);   // read again instead of held: the registers carry the sums
+      ring.get(1, g, valid);   // read again instead of held: the registers carry the sums
       const f2 r2 = both(r), mh = both(-(r * q[1] * inv));
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const f2 h = mul2(u[p], r2);
-        sw[p] = fma2(g[p], h, sw[p]);
+        if (ok) sw[p] = fma2(g[p], h, sw[p]);
         u[p] = mul2(r2, fma2(h, mh, a[p]));
       }
     }
     if constexpr (DROP) {
-      if (gz) {
+      if (A.grad_z) {
         f2 t[P];
-        ring.get(R - 1, t);
+        ring.get(R - 1, t, valid);
 #pragma unroll
         for (int p = 0; p < P; ++p) u[p] = add2(u[p], t[p]);
       }
-      if (gr) store<T, V, J>(gr + n * D.dim, u, lane, G, S, ok);
-      if (gx) apply_mask(u, mask.bits(drop, at, ch, (uint32_t)n), drop.scale);
+      if (gr && ok) gr.put(u, valid);
+      gr.next();
+      if (gx) apply_mask(u, mask.bits(drop, at, ch, n, valid), drop.scale);
     }
-    if (gx) store<T, V, J>(gx + n * D.dim, u, lane, G, S, ok);
+    if (gx && ok) gx.put(u, valid);
+    gx.next();
     ring.done();
   }
   ring.finish();
-  const int comps = WIDE ? B.d : 1;
   float* smem = reinterpret_cast<float*>(g_smem);
-  if (float* out = sums_out(M, B, at.k, comps, A.partial, A.grad_weight, B.chan0, false))
-    write_sums<V, J, WIDE>(sw, smem, out, at, ch);
+  if (float* out = sums_out(M, B, at.k, A.partial, A.grad_weight, B.chan0, false))
+    write_sums<V, J>(sw, smem, out, at, ch);
   if (centred)
-    if (float* out = sums_out(M, B, at.k, comps, A.partial, A.grad_bias, B.bias0, true))
-      write_sums<V, J, WIDE>(sb, smem, out, at, ch);
+    if (float* out = sums_out(M, B, at.k, A.partial, A.grad_bias, B.bias0, true))
+      write_sums<V, J>(sb, smem, out, at, ch);
 }
 
-template <class T, int V, int J, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? kWideMax : kThreads, WIDE ? 1 : 2)
+template <class T, int J, int TH, bool EDGE>
+TPC_NODE_KERNEL(TH, 2)
     k_dbl(const __grid_constant__ NodeDesc D, const __grid_constant__ RowMap M, const __grid_constant__ NormArgs A,
-          const long long N) {
-  constexpr int P = V * J / 2;
-  const Place<WIDE> at(D, M);
+          const uint32_t N) {
+  constexpr int V = 16 / sizeof(T), E = V * J, P = E / 2;
+  float* part = reinterpret_cast<float*>(g_smem + rows_bytes(E, 3, J, true, TH));
+  const Place<TH, EDGE> at(D, M, V, part);
   const NodeBlock& B = at.B;
-  const int S = B.S, G = at.G, lane = at.lane, S4 = (S + 3) / 4 * 4;
   const Channels ch(D, B);
   const bool centred = B.bias0 >= 0;
-  const float inv = 1.f / (float)S;
-  float* ws = reinterpret_cast<float*>(g_smem + rows_bytes(sizeof(T), V, V * J, 3, !WIDE, blockDim.x));
-  float *ts = ws + S4, *bs = ts + S4;
-  Ring<T, V, J, 3> ring;
-  ring.base[0] = (const T*)A.x + B.off;
-  ring.base[1] = (const T*)A.grad_y + B.off;
-  ring.base[2] = A.gg_x ? (const T*)A.gg_x + B.off : nullptr;
-  ring.start(g_smem, D, B, lane, G, at.n, at.stride, N);
-  expand(ws, A.weight ? A.weight + B.chan0 : nullptr, ch, S, 1.f);
-  expand(ts, A.gg_weight ? A.gg_weight + B.chan0 : nullptr, ch, S, 0.f);
-  expand(bs, centred && A.gg_bias ? A.gg_bias + B.bias0 : nullptr, ch, S, 0.f);
+  const float inv = 1.f / (float)B.S;
+  float* ws = reinterpret_cast<float*>(reinterpret_cast<char*>(part) + kPartBytes);
+  float *ts = ws + (E << at.lg), *bs = ts + (E << at.lg);
+  Ring<T, J, 3, TH, EDGE> ring;
+  ring.start(g_smem, D, at, N, {A.x, A.grad_y, A.gg_x});
+  expand(ws, E << at.lg, A.weight ? A.weight + B.chan0 : nullptr, ch, B.S, at.shift, 1.f);
+  expand(ts, E << at.lg, A.gg_weight ? A.gg_weight + B.chan0 : nullptr, ch, B.S, at.shift, 0.f);
+  expand(bs, E << at.lg, centred && A.gg_bias ? A.gg_bias + B.bias0 : nullptr, ch, B.S, at.shift, 0.f);
   __syncthreads();
+  const uint32_t valid = valid_bits<V, J>(at);
   f2 sw[P];
 #pragma unroll
   for (int p = 0; p < P; ++p) sw[p] = 0;
-  T *gx = A.grad_x ? (T*)A.grad_x + B.off : nullptr, *gg = A.grad_grad_y ? (T*)A.grad_grad_y + B.off : nullptr;
-  for (long long n = at.n; at.more(n, N); n += at.stride) {
+  Out<T, J, TH, EDGE> gx(A.grad_x, D, at), gg(A.grad_grad_y, D, at);
+  for (uint32_t n = at.n; at.more(n, N); n += at.stride) {
     const bool ok = n < N;
     ring.next();
     // u, p, a = weight g, e = gg_weight g; less their means in a 0e block
     f2 u[P], pt[P], a[P], e[P], w[P], t[P];
-    ring.get(0, u);
+    ring.get(0, u, valid);
     if (A.gg_x) {
-      ring.get(2, pt);
+      ring.get(2, pt, valid);
     } else {
 #pragma unroll
       for (int p = 0; p < P; ++p) pt[p] = 0;
     }
-    ring.get(1, a);
-    lookup<V, J>(w, ws, lane, G, S);
-    lookup<V, J>(t, ts, lane, G, S);
+    ring.get(1, a, valid);
+    lookup<V, J>(w, ws, at);
+    lookup<V, J>(t, ts, at);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       e[p] = mul2(a[p], t[p]);
@@ -635,10 +689,10 @@ __global__ void __launch_bounds__(WIDE ? kWideMax : kThreads, WIDE ? 1 : 2)
     if (centred) {
       float m[4] = {total(u), total(pt), total(a), total(e)};
       at.sum(m);
-      shift<V, J>(u, -m[0] * inv, lane, G, S);
-      shift<V, J>(pt, -m[1] * inv, lane, G, S);
-      shift<V, J>(a, -m[2] * inv, lane, G, S);
-      shift<V, J>(e, -m[3] * inv, lane, G, S);
+      shift_by<V, J, EDGE>(u, -m[0] * inv, valid);
+      shift_by<V, J, EDGE>(pt, -m[1] * inv, valid);
+      shift_by<V, J, EDGE>(a, -m[2] * inv, valid);
+      shift_by<V, J, EDGE>(e, -m[3] * inv, valid);
     }
     f2 q2[5];
 #pragma unroll
@@ -658,30 +712,38 @@ __global__ void __launch_bounds__(WIDE ? kWideMax : kThreads, WIDE ? 1 : 2)
     const float r = __frsqrt_rn(q[0] * inv + D.eps);
     const float mp = r * q[1] * inv, ma = r * q[2] * inv, mpa = q[3] * inv, me = r * q[4] * inv;
     // grad_x = h (r^2 (3 mp ma - mpa) - r me) - r^2 ma p - r^2 mp a + r e,  k = r (p - h mp)
-    const f2 r2 = both(r), ch_ = both(r * r * (3.f * mp * ma - mpa) - r * me), cp = both(-(r * r * ma)),
-             ca = both(-(r * r * mp)), nmp = both(-mp);
+    const f2 r2 = both(r), c_h = both(r * r * (3.f * mp * ma - mpa) - r * me), c_p = both(-(r * r * ma)),
+             c_a = both(-(r * r * mp)), nmp = both(-mp);
     f2 g[P], b[P];
-    ring.get(1, g);
-    lookup<V, J>(w, ws, lane, G, S);
-    lookup<V, J>(t, ts, lane, G, S);
-    lookup<V, J>(b, bs, lane, G, S);
+    ring.get(1, g, valid);
+    lookup<V, J>(w, ws, at);
+    lookup<V, J>(t, ts, at);
+    lookup<V, J>(b, bs, at);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const f2 h = mul2(u[p], r2), k = mul2(r2, fma2(h, nmp, pt[p]));
-      sw[p] = fma2(g[p], k, sw[p]);
-      u[p] = fma2(h, ch_, fma2(cp, pt[p], fma2(ca, a[p], mul2(r2, e[p]))));
+      if (ok) sw[p] = fma2(g[p], k, sw[p]);
+      u[p] = fma2(h, c_h, fma2(c_p, pt[p], fma2(c_a, a[p], mul2(r2, e[p]))));
       e[p] = fma2(w[p], k, fma2(t[p], h, b[p]));
     }
-    if (gx) store<T, V, J>(gx + n * D.dim, u, lane, G, S, ok);
-    if (gg) store<T, V, J>(gg + n * D.dim, e, lane, G, S, ok);
+    if (gx && ok) gx.put(u, valid);
+    if (gg && ok) gg.put(e, valid);
+    gx.next();
+    gg.next();
     ring.done();
   }
   ring.finish();
-  if (float* out = sums_out(M, B, at.k, WIDE ? B.d : 1, A.partial, A.grad_weight, B.chan0, false))
-    write_sums<V, J, WIDE>(sw, reinterpret_cast<float*>(g_smem), out, at, ch);
+  if (float* out = sums_out(M, B, at.k, A.partial, A.grad_weight, B.chan0, false))
+    write_sums<V, J>(sw, reinterpret_cast<float*>(g_smem), out, at, ch);
 }
 
 // ---- any width: one CTA per segment, read again for each sum; a thread owns whole channels ----
+
+template <int K>
+__device__ __forceinline__ void cta_sum(float (&v)[K], int& flip) {
+  __shared__ float part[2 * (kThreads / 32) * K];
+  warps_sum(v, part, flip, threadIdx.x >> 5, 0, kThreads / 32, kThreads / 32, [] { __syncthreads(); });
+}
 
 // The CTA's block and rows, as Place.
 struct AnyPlace {
@@ -707,8 +769,9 @@ __device__ __forceinline__ void each(const NodeBlock& B, int mul_ir, F f) {
 template <class T, bool DROP, bool NORM>
 __global__ void __launch_bounds__(kThreads)
     k_fwd_any(const __grid_constant__ NodeDesc D, const __grid_constant__ RowMap M, const __grid_constant__ Drop drop,
-              const __grid_constant__ NormArgs A, const long long N) {
+              const __grid_constant__ NormArgs A, const uint32_t N) {
   const AnyPlace at(D, M);
+  int flip = 0;
   const NodeBlock& B = at.B;
   const bool centred = B.bias0 >= 0;
   const float inv = 1.f / (float)B.S;
@@ -730,7 +793,7 @@ __global__ void __launch_bounds__(kThreads)
       if (centred) {
         float m[1] = {0.f};
         each(B, D.mul_ir, [&](int c, int s) { m[0] += value(c, s); });
-        cta_sum(m);
+        cta_sum(m, flip);
         mu = m[0] * inv;
       }
       float q[1] = {0.f};
@@ -738,7 +801,7 @@ __global__ void __launch_bounds__(kThreads)
         const float u = value(c, s) - mu;
         q[0] += u * u;
       });
-      cta_sum(q);
+      cta_sum(q, flip);
       r = __frsqrt_rn(q[0] * inv + D.eps);
     }
     each(B, D.mul_ir, [&](int c, int s) {
@@ -754,14 +817,15 @@ __global__ void __launch_bounds__(kThreads)
 template <class T, bool DROP>
 __global__ void __launch_bounds__(kThreads)
     k_bwd_any(const __grid_constant__ NodeDesc D, const __grid_constant__ RowMap M, const __grid_constant__ Drop drop,
-              const __grid_constant__ NormArgs A, const long long N) {
+              const __grid_constant__ NormArgs A, const uint32_t N) {
   const AnyPlace at(D, M);
+  int flip = 0;
   const NodeBlock& B = at.B;
   const bool centred = B.bias0 >= 0;
   const float inv = 1.f / (float)B.S;
   const uint64_t off = DROP ? drop_offset(drop) : 0;
-  float* pw = sums_out(M, B, at.k, 1, A.partial, A.grad_weight, B.chan0, false);
-  float* pb = centred ? sums_out(M, B, at.k, 1, A.partial, A.grad_bias, B.bias0, true) : nullptr;
+  float* pw = sums_out(M, B, at.k, A.partial, A.grad_weight, B.chan0, false);
+  float* pb = centred ? sums_out(M, B, at.k, A.partial, A.grad_bias, B.bias0, true) : nullptr;
   for (long long n = at.n; n < N; n += at.stride) {
     const long long row = n * D.dim + B.off;
     const T *x = (const T*)A.x + row, *g = (const T*)A.grad_y + row;
@@ -772,7 +836,7 @@ __global__ void __launch_bounds__(kThreads)
         m[0] += to_f32(x[s]);
         m[1] += a(c, s);
       });
-      cta_sum(m);
+      cta_sum(m, flip);
     }
     const float mu = m[0] * inv, ma = m[1] * inv;
     each(B, D.mul_ir, [&](int c, int s) {
@@ -780,7 +844,7 @@ __global__ void __launch_bounds__(kThreads)
       q[0] += u * u;
       q[1] += u * (a(c, s) - ma);
     });
-    cta_sum(q);
+    cta_sum(q, flip);
     const float r = __frsqrt_rn(q[0] * inv + D.eps), mh = r * q[1] * inv;
     for (int c = threadIdx.x; c < B.C; c += kThreads) {
       float sw = 0.f, sb = 0.f;
@@ -808,12 +872,13 @@ __global__ void __launch_bounds__(kThreads)
 template <class T>
 __global__ void __launch_bounds__(kThreads)
     k_dbl_any(const __grid_constant__ NodeDesc D, const __grid_constant__ RowMap M, const __grid_constant__ NormArgs A,
-              const long long N) {
+              const uint32_t N) {
   const AnyPlace at(D, M);
+  int flip = 0;
   const NodeBlock& B = at.B;
   const bool centred = B.bias0 >= 0;
   const float inv = 1.f / (float)B.S;
-  float* pw = sums_out(M, B, at.k, 1, A.partial, A.grad_weight, B.chan0, false);
+  float* pw = sums_out(M, B, at.k, A.partial, A.grad_weight, B.chan0, false);
   auto weight = [&](int c) { return A.weight ? A.weight[B.chan0 + c] : 1.f; };
   auto tangent = [&](int c) { return A.gg_weight ? A.gg_weight[B.chan0 + c] : 0.f; };
   for (long long n = at.n; n < N; n += at.stride) {
@@ -829,7 +894,7 @@ __global__ void __launch_bounds__(kThreads)
         m[2] += weight(c) * gv;
         m[3] += tangent(c) * gv;
       });
-      cta_sum(m);
+      cta_sum(m, flip);
     }
     const float mx = m[0] * inv, mp = m[1] * inv, ma = m[2] * inv, mw = m[3] * inv;
     each(B, D.mul_ir, [&](int c, int s) {
@@ -840,7 +905,7 @@ __global__ void __launch_bounds__(kThreads)
       q[3] += p * a;
       q[4] += u * (tangent(c) * gv - mw);
     });
-    cta_sum(q);
+    cta_sum(q, flip);
     const float r = __frsqrt_rn(q[0] * inv + D.eps);
     const float P = r * q[1] * inv, Q = r * q[2] * inv, R = q[3] * inv, W = r * q[4] * inv;
     for (int c = threadIdx.x; c < B.C; c += kThreads) {
@@ -887,15 +952,11 @@ __global__ void __launch_bounds__(32 * kShares)
     wanted = k < M.n;  // else the block's only CTA has written the gradient
     if (wanted) {
       const NodeBlock& B = D.b[M.blk[k]];
-      const int comps = bias ? 1 : M.comps[k], parts = M.parts[k];
-      const long long stride = part_stride(B, M.comps[k]);
-      const float* p = partial + M.part0[k] + (bias ? (long long)B.C * M.comps[k] : 0);
-      const int own = c - (bias ? B.bias0 : B.chan0);
-      for (int m = 0; m < comps; ++m) {
-        const float* q = p + (D.mul_ir ? own * comps + m : m * B.C + own);
-#pragma unroll 4
-        for (int t = ty; t < parts; t += kShares) v += q[t * stride];
-      }
+      const int parts = M.parts[k];
+      const long long stride = part_stride(B);
+      const float* q = partial + M.part0[k] + (bias ? B.C + c - B.bias0 : c - B.chan0);
+#pragma unroll 8
+      for (int t = ty; t < parts; t += kShares) v += q[t * stride];
     }
   }
   share[ty][tx] = v;
@@ -911,6 +972,9 @@ __global__ void __launch_bounds__(32 * kShares)
 
 // ---- launch plan ----
 
+enum Pass { PASS_FWD = NORM_FORWARD, PASS_BWD = NORM_BACKWARD, PASS_DBL = NORM_DOUBLE_BACKWARD };
+enum Kind { KIND_GROUP, KIND_WIDE, KIND_ANY };  // 256 threads, one group of 512, any width
+
 struct Launch {
   Kind kind;
   int J, ctas, threads, smem;
@@ -918,134 +982,134 @@ struct Launch {
 };
 
 struct LaunchPlan {
-  int V = 1, n = 0;
+  bool edge = false;
+  int n = 0;
   Launch l[3];
   PartMap parts{};
   size_t floats = 0;   // partial sums
 };
 
-// Elements of one access: 16 bytes where every block starts and ends on that boundary (rows then do,
-// too), else pairs of 16-bit values, else single elements.
-int pack_width(const NodeDesc& D, int esize) {
-  for (int V : {16 / esize, 2, 1}) {
-    if (V * esize > 16 || (esize == 4 && V == 2)) continue;
-    bool fits = true;
-    for (int b = 0; b < D.n_blocks; ++b) fits = fits && D.b[b].S % V == 0;
-    if (fits) return V;
-  }
-  return 1;
-}
+// Packs per lane that the kernels are built for: 1..most (run_pass).  At most 16 elements a lane, 12
+// (8 in 16 bits) in the double backward, whose five values per element fill the registers.
+constexpr int most_packs(bool dbl, int esize) { return dbl ? (esize == 4 ? 3 : 1) : (esize == 4 ? 4 : 2); }
 
-enum Pass { PASS_FWD = NORM_FORWARD, PASS_BWD = NORM_BACKWARD, PASS_DBL = NORM_DOUBLE_BACKWARD };
-
-// Packs per lane that the kernels are built for (run_width), ascending, ending with 0.
-const int* pack_counts(Pass pass, int V) {
-  static const int f4[] = {1, 2, 3, 4, 5, 0}, f8[] = {1, 2, 3, 0}, f2[] = {4, 8, 0}, f1[] = {4, 8, 16, 0};
-  static const int d4[] = {1, 2, 3, 0}, d8[] = {1, 2, 0}, d2[] = {4, 0}, d1[] = {4, 8, 0};
-  if (pass == PASS_DBL) return V == 4 ? d4 : V == 8 ? d8 : V == 2 ? d2 : d1;
-  return V == 4 ? f4 : V == 8 ? f8 : V == 2 ? f2 : f1;
-}
-constexpr int wide_packs(bool dbl, int V) { return (dbl ? 8 : 16) / V; }
-
-int log2_lanes(int S, int per_lane) {
+int log2_lanes(int elems, int per_lane) {
   int lg = 0;
-  while ((per_lane << lg) < S) ++lg;
+  while ((per_lane << lg) < elems) ++lg;
   return lg;
 }
 
-// Dynamic shared memory of a CTA whose widest segment has S elements.
-int smem_bytes(Pass pass, bool drop, bool norm, int esize, int V, int J, int threads, bool wide, int S) {
-  const int arrays = pass == PASS_FWD ? (drop ? 2 : 1) : pass == PASS_BWD ? (drop ? 3 : 2) : 3;
-  const int vectors = pass == PASS_FWD ? (norm ? 2 : 0) : pass == PASS_BWD ? 1 : 3;
-  return rows_bytes(esize, V, V * J, arrays, pass != PASS_FWD && !wide, threads) + vectors * vector_bytes(S) +
-         (drop ? mask_bytes(V * J, threads) : 0);
-}
+struct Shape {
+  Pass pass;
+  bool drop, norm;
+  int esize, V;
+  int arrays() const { return pass == PASS_FWD ? (drop ? 2 : 1) : pass == PASS_BWD ? (drop ? 3 : 2) : 3; }
+  // Dynamic shared memory of a CTA whose widest group has 2^lg lanes.
+  int smem(int J, int threads, int lg) const {
+    const int vectors = pass == PASS_FWD ? (norm ? 2 : 0) : pass == PASS_BWD ? 1 : 3;
+    return rows_bytes(V * J, arrays(), J, pass != PASS_FWD, threads) + kPartBytes +
+           vectors * vector_bytes(V * J, lg) + (drop ? mask_bytes(V * J, threads) : 0);
+  }
+};
 
-// CTAs that an SM holds: by registers (launch bounds; more where the kernels use fewer) and by
-// shared memory (227 KB, 1 KB of it per CTA for the system).
+// CTAs that an SM holds: by registers and by shared memory (227 KB, 1 KB of it per CTA for the
+// system).
 int ctas_per_sm(int by_registers, int smem) {
-  const int by_smem = 232448 / (smem + 1024 + 512);
+  const int by_smem = 232448 / (smem + 1024);
   return by_smem < 1 ? 1 : by_smem < by_registers ? by_smem : by_registers;
 }
 
-LaunchPlan plan_launches(Pass pass, bool drop, bool norm, const NodeDesc& D, long long N, int esize) {
+LaunchPlan plan_launches(const Shape& sh, const NodeDesc& D, long long N) {
   LaunchPlan P;
-  P.V = pack_width(D, esize);
-  const int* js = pack_counts(pass, P.V);
-  int jmax = 0;
-  for (const int* j = js; *j; ++j) jmax = *j;
-  const int jw = wide_packs(pass == PASS_DBL, P.V);
+  const int V = sh.V;
+  const bool sums = sh.pass != PASS_FWD;
+  for (int b = 0; b < D.n_blocks; ++b) P.edge = P.edge || D.b[b].S % V != 0;
+  int R = 1;  // rows after which a row starts on the same offset from a 16-byte boundary
+  while (P.edge && (long long)R * D.dim % V != 0) R *= 2;
+  const int pad = P.edge ? V - 1 : 0;
+  const int jmax = most_packs(sh.pass == PASS_DBL, sh.esize);
   Kind kind[MAX_BLOCKS];
-  const auto wide_threads = [&](int S) { return (S + 32 * P.V * jw - 1) / (32 * P.V * jw) * 32; };
-  const auto wide_smem = [&](int S) { return smem_bytes(pass, drop, norm, esize, P.V, jw, wide_threads(S), true, S); };
   for (int b = 0; b < D.n_blocks; ++b) {
-    const int S = D.b[b].S;
-    kind[b] = S <= 32 * P.V * jmax                                           ? KIND_GROUP
-              : S <= kWideMax * P.V * jw && wide_smem(S) <= kMaxSmem ? KIND_WIDE
-                                                                             : KIND_ANY;
+    const int S = D.b[b].S + pad;
+    kind[b] = S <= kThreads * V * jmax                                                         ? KIND_GROUP
+              : S <= kWide * V * jmax && sh.smem(jmax, kWide, log2_lanes(kWide, 1)) <= kMaxSmem ? KIND_WIDE
+                                                                                               : KIND_ANY;
   }
   for (Kind kd : {KIND_GROUP, KIND_WIDE, KIND_ANY}) {
     Launch L{};
     L.kind = kd;
-    long long total = 0;
-    int widest = 0;
+    RowMap& M = L.M;
     for (int b = 0; b < D.n_blocks; ++b)
-      if (kind[b] == kd) {
-        L.M.blk[L.M.n++] = b;
-        total += D.b[b].S;
-        widest = D.b[b].S > widest ? D.b[b].S : widest;
-      }
-    if (L.M.n == 0) continue;
+      if (kind[b] == kd) M.blk[M.n++] = b;
+    if (M.n == 0) continue;
+    L.threads = kd == KIND_WIDE ? kWide : kThreads;
+    M.classes = kd == KIND_ANY ? 1 : R;
     long long resident;   // CTAs that run at a time
-    L.threads = kThreads;
-    if (kd == KIND_GROUP) {
+    if (kd == KIND_ANY) {
+      resident = sums ? kAnyParts : kSms * 8;
+      for (int k = 0; k < M.n; ++k) M.lg[k] = log2_lanes(kThreads, 1);
+    } else {
       // fewest lane-packs per row; a segment's lanes are a power of two
+      const int lg_max = log2_lanes(L.threads, 1);
       long long best = -1;
-      for (const int* j = js; *j; ++j) {
-        if (widest > 32 * P.V * *j) continue;
+      for (int j = kd == KIND_WIDE ? jmax : 1; j <= jmax; ++j) {
         long long cost = 0;
-        for (int k = 0; k < L.M.n; ++k) cost += (long long)*j << log2_lanes(D.b[L.M.blk[k]].S, P.V * *j);
-        if (best < 0 || cost <= best) {
+        bool fits = true;
+        for (int k = 0; k < M.n; ++k) {
+          const int lg = log2_lanes(D.b[M.blk[k]].S + pad, V * j);
+          fits = fits && lg <= lg_max;
+          cost += (long long)j << lg;
+        }
+        if (fits && (best < 0 || cost <= best)) {
           best = cost;
-          L.J = *j;
+          L.J = j;
         }
       }
-      for (int k = 0; k < L.M.n; ++k) L.M.lg[k] = log2_lanes(D.b[L.M.blk[k]].S, P.V * L.J);
-      L.smem = smem_bytes(pass, drop, norm, esize, P.V, L.J, L.threads, false, widest);
-      resident = kSms * ctas_per_sm(pass == PASS_FWD ? 4 : 2, L.smem);
-    } else if (kd == KIND_WIDE) {
-      L.J = jw;
-      L.threads = wide_threads(widest);
-      L.smem = wide_smem(widest);
-      resident = kSms * ctas_per_sm(kWideMax / L.threads, L.smem);
-    } else {
-      resident = pass == PASS_FWD ? kSms * 8 : kAnyParts;
-    }
-    bool direct = pass != PASS_FWD;
-    for (int k = 0; k < L.M.n; ++k) {
-      const NodeBlock& B = D.b[L.M.blk[k]];
-      const long long rows = kd == KIND_GROUP ? kThreads >> L.M.lg[k] : 1;
-      const long long most = (N + rows - 1) / rows;
-      long long ctas = resident * B.S / total;
-      if (pass != PASS_FWD) {
-        if (kd == KIND_ANY && ctas > kAnyFloats / part_stride(B, 1)) ctas = kAnyFloats / part_stride(B, 1);
-        if (most <= 8) ctas = 1;
+      int widest = 0;
+      for (int k = 0; k < M.n; ++k) {
+        M.lg[k] = kd == KIND_WIDE ? lg_max : log2_lanes(D.b[M.blk[k]].S + pad, V * L.J);
+        widest = M.lg[k] > widest ? M.lg[k] : widest;
       }
-      ctas = ctas < 1 ? 1 : ctas > most ? most : ctas;
-      L.M.cta0[k + 1] = L.M.cta0[k] + (int)ctas;
-      direct = direct && ctas == 1 && (kd != KIND_WIDE || B.d == 1);  // WIDE sums are per element
+      L.smem = sh.smem(L.J, L.threads, widest);
+      resident = kSms * ctas_per_sm(kd == KIND_WIDE ? 1 : 2, L.smem);
     }
-    L.ctas = L.M.cta0[L.M.n];
-    L.M.direct = direct;
-    if (pass != PASS_FWD && !direct)
-      for (int k = 0; k < L.M.n; ++k) {
-        const NodeBlock& B = D.b[L.M.blk[k]];
-        const int i = P.parts.n++, comps = kd == KIND_WIDE ? B.d : 1;
-        P.parts.blk[i] = L.M.blk[k];
-        P.parts.parts[i] = L.M.cta0[k + 1] - L.M.cta0[k];
-        P.parts.comps[i] = comps;
-        P.parts.part0[i] = L.M.part0[k] = (long long)P.floats;
-        P.floats += (size_t)(P.parts.parts[i] * part_stride(B, comps));
+    // Steps of a CTA: as few as let all CTAs run at a time.  Few rows: one CTA per block, whose sums
+    // need no second launch.
+    long long rows[MAX_BLOCKS], total = 0, most = 0;   // rows[k]: CTA steps of block k in a residue class
+    for (int k = 0; k < M.n; ++k) {
+      const int per_step = kd == KIND_ANY ? 1 : L.threads >> M.lg[k];
+      rows[k] = ((N + M.classes - 1) / M.classes + per_step - 1) / per_step;
+      total += rows[k] * M.classes;
+      most = rows[k] > most ? rows[k] : most;
+    }
+    long long steps = (total + resident - 1) / resident;
+    if (steps < 1) steps = 1;
+    const auto ctas = [&](int k) { return (rows[k] + steps - 1) / steps * M.classes; };
+    if (sums && M.classes == 1 && most <= 8) {
+      steps = most;
+    } else {
+      for (;; steps += steps / 32 + 1) {
+        long long c = 0;
+        for (int k = 0; k < M.n; ++k) c += ctas(k);
+        if (c <= resident || steps >= most) break;
+      }
+    }
+    M.direct = sums;
+    for (int k = 0; k < M.n; ++k) {
+      long long c = ctas(k);
+      const long long room = kAnyFloats / part_stride(D.b[M.blk[k]]);
+      if (sums && kd == KIND_ANY && c > room) c = room < 1 ? 1 : room;
+      M.cta0[k + 1] = M.cta0[k] + (int)c;
+      M.direct = M.direct && c == 1;
+    }
+    L.ctas = M.cta0[M.n];
+    if (sums && !M.direct)
+      for (int k = 0; k < M.n; ++k) {
+        const int i = P.parts.n++;
+        P.parts.blk[i] = M.blk[k];
+        P.parts.parts[i] = M.cta0[k + 1] - M.cta0[k];
+        P.parts.part0[i] = M.part0[k] = (long long)P.floats;
+        P.floats += (size_t)(P.parts.parts[i] * part_stride(D.b[M.blk[k]]));
       }
     P.l[P.n++] = L;
   }
@@ -1059,7 +1123,7 @@ struct Call {
   const NodeDesc& D;
   const Drop& d;
   const NormArgs& A;
-  long long N;
+  uint32_t N;
   cudaStream_t s;
 };
 
@@ -1079,45 +1143,35 @@ void launch(void (*kernel)(Ps...), std::atomic<uint64_t>& allowed, const Call& c
   kernel<<<L.ctas, L.threads, L.smem, c.s>>>(args...);
 }
 
-template <class T, int V, int J, bool WIDE, bool DBL>
-void run_packs(const Call& c, const Launch& L) {
-  static std::atomic<uint64_t> ok[5];  // devices, by kernel
-  if constexpr (DBL) {
-    launch(k_dbl<T, V, J, WIDE>, ok[0], c, L, c.D, L.M, c.A, c.N);
-  } else if (c.pass == PASS_FWD) {
-    if (c.drop && c.norm) launch(k_fwd<T, V, J, WIDE, true, true>, ok[0], c, L, c.D, L.M, c.d, c.A, c.N);
-    else if (c.drop) launch(k_fwd<T, V, J, WIDE, true, false>, ok[1], c, L, c.D, L.M, c.d, c.A, c.N);
-    else launch(k_fwd<T, V, J, WIDE, false, true>, ok[2], c, L, c.D, L.M, c.d, c.A, c.N);
-  } else {
-    if (c.drop) launch(k_bwd<T, V, J, WIDE, true>, ok[3], c, L, c.D, L.M, c.d, c.A, c.N);
-    else launch(k_bwd<T, V, J, WIDE, false>, ok[4], c, L, c.D, L.M, c.d, c.A, c.N);
+template <class T, int J, int TH, bool EDGE>
+void run_kernel(const Call& c, const Launch& L) {
+  constexpr bool dbl = J <= most_packs(true, sizeof(T));
+  static std::atomic<uint64_t> ok[6];  // devices, by kernel
+  if (c.pass == PASS_FWD) {
+    if (c.drop && c.norm) launch(k_fwd<T, J, TH, EDGE, true, true>, ok[0], c, L, c.D, L.M, c.d, c.A, c.N);
+    else if (c.drop) launch(k_fwd<T, J, TH, EDGE, true, false>, ok[1], c, L, c.D, L.M, c.d, c.A, c.N);
+    else launch(k_fwd<T, J, TH, EDGE, false, true>, ok[2], c, L, c.D, L.M, c.d, c.A, c.N);
+  } else if (c.pass == PASS_BWD) {
+    if (c.drop) launch(k_bwd<T, J, TH, EDGE, true>, ok[3], c, L, c.D, L.M, c.d, c.A, c.N);
+    else launch(k_bwd<T, J, TH, EDGE, false>, ok[4], c, L, c.D, L.M, c.d, c.A, c.N);
+  } else if constexpr (dbl) {
+    launch(k_dbl<T, J, TH, EDGE>, ok[5], c, L, c.D, L.M, c.A, c.N);
   }
 }
 
-// the kernel of a launch's pack count, out of pack_counts
-template <class T, int V, bool DBL, int... Js>
-void run_counts(const Call& c, const Launch& L) {
-  ((L.J == Js ? run_packs<T, V, Js, false, DBL>(c, L) : void()), ...);
-}
-
-template <class T, int V>
-void run_width(const Call& c, const Launch& L) {
-  const bool dbl = c.pass == PASS_DBL;
+template <class T, bool EDGE>
+void run_packs(const Call& c, const Launch& L) {
+  constexpr int most = most_packs(false, sizeof(T)), dbl = most_packs(true, sizeof(T));
   if (L.kind == KIND_WIDE) {
-    if (dbl) run_packs<T, V, wide_packs(true, V), true, true>(c, L);
-    else run_packs<T, V, wide_packs(false, V), true, false>(c, L);
-  } else if constexpr (V == 4) {
-    if (dbl) run_counts<T, V, true, 1, 2, 3>(c, L);
-    else run_counts<T, V, false, 1, 2, 3, 4, 5>(c, L);
-  } else if constexpr (V == 8) {
-    if (dbl) run_counts<T, V, true, 1, 2>(c, L);
-    else run_counts<T, V, false, 1, 2, 3>(c, L);
-  } else if constexpr (V == 2) {
-    if (dbl) run_counts<T, V, true, 4>(c, L);
-    else run_counts<T, V, false, 4, 8>(c, L);
-  } else {
-    if (dbl) run_counts<T, V, true, 4, 8>(c, L);
-    else run_counts<T, V, false, 4, 8, 16>(c, L);
+    if (L.J == most) run_kernel<T, most, kWide, EDGE>(c, L);
+    else run_kernel<T, dbl, kWide, EDGE>(c, L);
+    return;
+  }
+  if (L.J == 1) run_kernel<T, 1, kThreads, EDGE>(c, L);
+  if (L.J == 2) run_kernel<T, 2, kThreads, EDGE>(c, L);
+  if constexpr (most == 4) {
+    if (L.J == 3) run_kernel<T, 3, kThreads, EDGE>(c, L);
+    if (L.J == 4) run_kernel<T, 4, kThreads, EDGE>(c, L);
   }
 }
 
@@ -1138,17 +1192,16 @@ void run_any(const Call& c, const Launch& L) {
 
 template <class T>
 cudaError_t run_node(const Call& c) {
-  const LaunchPlan P = plan_launches(c.pass, c.drop, c.norm, c.D, c.N, sizeof(T));
+  const LaunchPlan P = plan_launches(Shape{c.pass, c.drop, c.norm, sizeof(T), 16 / sizeof(T)}, c.D, c.N);
   for (int i = 0; i < P.n; ++i) {
     const Launch& L = P.l[i];
     if (L.kind == KIND_ANY) run_any<T>(c, L);
-    else if (P.V == 16 / (int)sizeof(T)) run_width<T, 16 / (int)sizeof(T)>(c, L);
-    else if (P.V == 1) run_width<T, 1>(c, L);
-    else if constexpr (sizeof(T) == 2) run_width<T, 2>(c, L);
+    else if (P.edge) run_packs<T, true>(c, L);
+    else run_packs<T, false>(c, L);
   }
   if (c.A.partial && P.parts.n)
-    k_norm_reduce<<<(c.D.channels + c.D.biases + 31) / 32, 32 * kShares, 0, c.s>>>(c.D, P.parts, c.A.partial, c.A.grad_weight,
-                                                                          c.A.grad_bias);
+    k_norm_reduce<<<(c.D.channels + c.D.biases + 31) / 32, 32 * kShares, 0, c.s>>>(c.D, P.parts, c.A.partial,
+                                                                                 c.A.grad_weight, c.A.grad_bias);
   return cudaGetLastError();
 }
 
@@ -1172,7 +1225,7 @@ cudaError_t run_node_f16(TPC_NODE_ARGS);
 #endif
 cudaError_t TPC_RUN(TPC_NODE_ARGS) {
   const Drop none{};
-  return run_node<TPC_T>(Call{(Pass)pass, drop != nullptr, norm, D, drop ? *drop : none, A, N, s});
+  return run_node<TPC_T>(Call{(Pass)pass, drop != nullptr, norm, D, drop ? *drop : none, A, (uint32_t)N, s});
 }
 
 #if TPC_UNIT_T == 0
@@ -1199,10 +1252,11 @@ cudaError_t launch_dropout(int dtype, const NodeDesc& D, long long N, const void
 size_t norm_partial_floats(const NodeDesc& D, long long N, int esize) {
   if (N == 0) return 0;
   size_t most = 0;
-  for (const LaunchPlan& P :
-       {plan_launches(PASS_BWD, false, true, D, N, esize), plan_launches(PASS_BWD, true, true, D, N, esize),
-        plan_launches(PASS_DBL, false, true, D, N, esize)})
-    most = P.floats > most ? P.floats : most;
+  for (const Shape& sh : {Shape{PASS_BWD, false, true, esize, 16 / esize}, Shape{PASS_BWD, true, true, esize, 16 / esize},
+                          Shape{PASS_DBL, false, true, esize, 16 / esize}}) {
+    const size_t f = plan_launches(sh, D, N).floats;
+    most = f > most ? f : most;
+  }
   return most;
 }
 #endif

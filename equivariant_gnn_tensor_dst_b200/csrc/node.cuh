@@ -55,11 +55,32 @@ __device__ __forceinline__ float drop_one(const Drop& D, uint64_t off, const Nod
   return word_of(w, c & 3) >= D.threshold ? __fmul_rn(v, D.scale) : 0.f;
 }
 
-// V consecutive elements, loaded and stored in one access.
-template <class T, int V>
-struct alignas(sizeof(T) * V) Pack {
-  T v[V];
-};
+// Two 16-bit elements of a word, lower address first.
+template <class T>
+__device__ __forceinline__ void unpack(uint32_t w, float& x, float& y);
+template <>
+__device__ __forceinline__ void unpack<__nv_bfloat16>(uint32_t w, float& x, float& y) {
+  x = __uint_as_float(w << 16);
+  y = __uint_as_float(w & 0xffff0000u);
+}
+template <>
+__device__ __forceinline__ void unpack<__half>(uint32_t w, float& x, float& y) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  x = f.x;
+  y = f.y;
+}
+template <class T>
+__device__ __forceinline__ uint32_t pack(float x, float y);
+template <>
+__device__ __forceinline__ uint32_t pack<__nv_bfloat16>(float x, float y) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack<__half>(float x, float y) {
+  const __half2 v = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 
 // Which channels of a block the elements s (block-relative) belong to.
 struct Channels {

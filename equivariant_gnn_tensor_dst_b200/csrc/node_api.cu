@@ -1,6 +1,7 @@
 // C ABI of the node-feature operators (include/tpconv_node.h): plans, argument checks and
 // launches.
 #include <cmath>
+#include <mutex>
 #include <new>
 #include <vector>
 
@@ -14,6 +15,10 @@ using namespace tpc;
 struct tpconv_node_plan {
   NodeDesc desc{};
   int dtype = TPCONV_DTYPE_F32;
+  // workspace of the last row count asked for (host bookkeeping: a training loop asks for the same)
+  mutable std::mutex mu;
+  mutable int64_t ws_rows = -1;
+  mutable size_t ws_bytes = 0;
 };
 
 namespace {
@@ -70,10 +75,19 @@ tpconv_status make_drop(const tpconv_dropout_spec* spec, Drop& d) {
   return TPCONV_OK;
 }
 
+size_t sums_bytes(const tpconv_node_plan* P, int64_t N) {
+  std::lock_guard<std::mutex> g(P->mu);
+  if (P->ws_rows != N) {
+    P->ws_bytes = sizeof(float) * norm_partial_floats(P->desc, N, (int)elem_bytes(P));
+    P->ws_rows = N;
+  }
+  return P->ws_bytes;
+}
+
 // Bytes of the workspace that a pass writes, for the overlap check (one that is too small is
 // reported as that).
 size_t ws_span(const tpconv_node_plan* P, int64_t N, size_t ws_bytes) {
-  const size_t need = sizeof(float) * norm_partial_floats(P->desc, N, (int)elem_bytes(P));
+  const size_t need = sums_bytes(P, N);
   return ws_bytes < need ? ws_bytes : need;
 }
 
@@ -82,7 +96,7 @@ tpconv_status sums_workspace(const tpconv_node_plan* P, int64_t N, bool wanted, 
                              float** partial) {
   *partial = nullptr;
   if (!wanted || N == 0) return TPCONV_OK;
-  const size_t need = sizeof(float) * norm_partial_floats(P->desc, N, (int)elem_bytes(P));
+  const size_t need = sums_bytes(P, N);
   if (ws_bytes < need) return TPCONV_ERR_WORKSPACE_TOO_SMALL;
   if (need == 0) return TPCONV_OK;  // few rows: the sums go to the gradients themselves
   if (!ws) return TPCONV_ERR_INVALID_ARG;
@@ -169,7 +183,7 @@ tpconv_status tpconv_node_plan_set_layout(tpconv_node_plan_t P, int32_t layout) 
 
 tpconv_status tpconv_node_workspace_bytes(tpconv_node_plan_t P, int64_t N, size_t* bytes) {
   if (!bytes || !rows_ok(P, N)) return TPCONV_ERR_INVALID_ARG;
-  *bytes = sizeof(float) * norm_partial_floats(P->desc, N, (int)elem_bytes(P));
+  *bytes = sums_bytes(P, N);
   return TPCONV_OK;
 }
 
