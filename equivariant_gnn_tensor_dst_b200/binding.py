@@ -536,6 +536,11 @@ def _node_ptrs(plan, x, name, rows, params):
     return ptrs
 
 
+def _channel_sums(weight, n, device):
+    import torch
+    return torch.empty_like(weight) if weight is not None else torch.empty(n, dtype=torch.float32, device=device)
+
+
 def _node_call(device, name, stream, *args):
     """One library call on the tensors' device and the given (or that device's current) stream."""
     import torch
@@ -574,7 +579,7 @@ def tpconv_norm_backward(plan, x, weight, grad_y, need_x=True, need_weight=True,
     dev, N = x.device, x.shape[0]
     if outputs is None:
         gx = torch.empty_like(x) if need_x else None
-        gw = torch.empty(plan.channels, dtype=torch.float32, device=dev) if need_weight else None
+        gw = _channel_sums(weight, plan.channels, dev) if need_weight else None
         gb = torch.empty(plan.biases, dtype=torch.float32, device=dev) if need_bias else None
     else:
         gx, gw, gb = outputs
@@ -593,7 +598,7 @@ def tpconv_norm_double_backward(plan, x, weight, grad_y, gg_x=None, gg_weight=No
     dev, N = x.device, x.shape[0]
     if outputs is None:
         gx = torch.empty_like(x) if need_x else None
-        gw = torch.empty(plan.channels, dtype=torch.float32, device=dev) if need_weight else None
+        gw = _channel_sums(weight, plan.channels, dev) if need_weight else None
         gg = torch.empty_like(x) if need_grad_y else None
     else:
         gx, gw, gg = outputs
@@ -647,7 +652,7 @@ def tpconv_dropout_norm_backward(plan, z, weight, grad_y, dropout, grad_z=None, 
     if outputs is None:
         gx = torch.empty_like(z) if need_x else None
         gr = torch.empty_like(z) if need_residual else None
-        gw = torch.empty(plan.channels, dtype=torch.float32, device=dev) if need_weight else None
+        gw = _channel_sums(weight, plan.channels, dev) if need_weight else None
         gb = torch.empty(plan.biases, dtype=torch.float32, device=dev) if need_bias else None
     else:
         gx, gr, gw, gb = outputs

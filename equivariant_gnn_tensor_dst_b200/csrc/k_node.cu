@@ -22,6 +22,7 @@
 // Sums over rows (weight and bias gradients) have no atomics: each CTA writes its partial sums to
 // the workspace and k_norm_reduce adds them in CTA order; a launch with one CTA per block writes
 // the gradients itself.
+#include <algorithm>
 #include <atomic>
 
 #include "node.cuh"
@@ -32,6 +33,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWide = 512;         // threads of a CTA whose only group is beyond 256 lanes
 constexpr int kSms = 148;
+constexpr int kDropCtas = 4;       // CTAs per SM of k_drop
 constexpr int kMaxSmem = 231 * 1000;  // dynamic shared memory of a CTA (the rest of 227 KB is static)
 constexpr int kAnyParts = 296;     // row ranges of the any-width kernels
 constexpr int kAnyFloats = 1 << 22;  // bound on their partial sums
@@ -86,13 +88,17 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
 }
 template <int P>
 __device__ __forceinline__ float total(const f2 (&v)[P]) {
-  f2 s = v[0];
+  f2 s[P];
 #pragma unroll
-  for (int p = 1; p < P; ++p) s = add2(s, v[p]);
-  return lo(s) + hi(s);
+  for (int p = 0; p < P; ++p) s[p] = v[p];
+#pragma unroll
+  for (int n = P; n > 1; n = (n + 1) / 2)
+#pragma unroll
+    for (int p = 0; p < n / 2; ++p) s[p] = add2(s[p], s[n - 1 - p]);
+  return lo(s[0]) + hi(s[0]);
 }
 
-// Sums of K values over W consecutive warps (each thread's own values), to all their threads, by
+// Sums of K values over W (a power of two) consecutive warps, to all their threads, by
 // way of part[2][warps of the CTA][K] in shared memory: calls alternate between the two halves, and
 // none can be two calls ahead of another warp, so one barrier a call is enough.
 template <int K, class Sync>
@@ -105,11 +111,10 @@ __device__ __forceinline__ void warps_sum(float (&v)[K], float* part, int& flip,
 #pragma unroll
     for (int k = 0; k < K; ++k) half[warp * K + k] = v[k];
   sync();
+  const int w = first + ((int)threadIdx.x & (W - 1));
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = 0.f;
-  for (int w = first; w < first + W; ++w)
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += half[w * K + k];
+  for (int k = 0; k < K; ++k) v[k] = half[w * K + k];
+  group_sum(v, W);
 }
 
 // ---- segments in registers ----
@@ -160,10 +165,12 @@ struct Place {
   __device__ __forceinline__ int elem(int j) const { return (j * G + lane) * V - shift; }
 };
 
-// Slots of the copy ring: enough that a CTA has 16 KB or more on the way (as measured, more gains
-// nothing), two at least.
-__host__ __device__ constexpr int ring_slots(int pack_bytes) {
-  return pack_bytes * kThreads >= 16384 ? 2 : pack_bytes * kThreads >= 8192 ? 3 : 4;
+// Slots of the copy ring.  A CTA keeps 12 KB of rows on the way in float32 (forward 50000 x 592: 41 us,
+// 47 us with 24 KB or more), 24 KB in 16 bits, where a row is half as long and takes as many
+// instructions (the same in bf16: 31 us with one row ahead, 26 us with 12 KB, 25 us with 24 KB).
+__host__ __device__ constexpr int ring_slots(int esize, int pack_bytes) {
+  const int rows = ((esize == 4 ? 12288 : 24576) + pack_bytes * kThreads - 1) / (pack_bytes * kThreads);
+  return rows > 7 ? 8 : rows + 1;
 }
 
 // A thread's own packs of A arrays, copied ahead row by row.  Packs beyond the segment hold zeros
@@ -171,13 +178,14 @@ __host__ __device__ constexpr int ring_slots(int pack_bytes) {
 // groups that share a warp with others, but neither stored nor summed).
 template <class T, int J, int A, int TH, bool EDGE>
 struct Ring {
-  static constexpr int V = 16 / sizeof(T), kSlots = ring_slots(16 * A * J);
-  static constexpr int kPack = 16 * TH, kSlot = A * J * kPack, kBytes = kSlots * kSlot;
+  static constexpr int V = 16 / sizeof(T), kSlots = ring_slots(sizeof(T), 16 * A * J);
+  static constexpr int kPack = 16 * TH, kSlot = A * J * kPack;
   const char* p[A];          // this lane's pack 0 in the row `ahead`; NULL: no such array
   uint32_t mine, fill, read; // shared addresses: slot 0, next slot to fill, current slot
   uint32_t ahead, N, stride;
   uint32_t inside;           // bit j: pack j has elements of the segment
-  long long row_step, pack_step;
+  long long row_step;
+  uint32_t pack_step;        // bytes between a lane's packs
   long long left;            // EDGE: bytes from p[] to the end of the arrays
 
   __device__ __forceinline__ void start(char* smem, const NodeDesc& D, const Place<TH, EDGE>& at, uint32_t N_,
@@ -188,7 +196,7 @@ struct Ring {
     stride = at.stride;
     const long long first = (long long)ahead * D.dim + at.B.off + at.template elem<V>(0);
     row_step = (long long)stride * D.dim * (int)sizeof(T);
-    pack_step = (long long)at.step * (int)sizeof(T);
+    pack_step = at.step * (uint32_t)sizeof(T);
     left = ((long long)N * D.dim - first) * (int)sizeof(T);
 #pragma unroll
     for (int a = 0; a < A; ++a) p[a] = arrays[a] ? (const char*)arrays[a] + first * (int)sizeof(T) : nullptr;
@@ -237,15 +245,51 @@ struct Ring {
     issue();
     asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
   }
-  // pairs of array a of the current row; EDGE: `valid` marks the elements of the segment
-  __device__ __forceinline__ void get(int a, f2 (&v)[V * J / 2], uint32_t valid) const {
+  // pack j of array a of the current row
+  __device__ __forceinline__ uint4 word(int a, int j) const {
+    uint4 w;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                 : "r"(read + (a * J + j) * kPack)
+                 : "memory");
+    return w;
+  }
+  __device__ __forceinline__ void done() { read = read == mine + (kSlots - 1) * kSlot ? mine : read + kSlot; }
+  __device__ __forceinline__ void finish() const { asm volatile("cp.async.wait_all;" ::: "memory"); }
+};
+
+// Pairs of array a of the current row.  EDGE: `inner` masks the words of the packs to the elements
+// of the segment.
+template <class T, int J, bool EDGE>
+struct Inner {
+  static constexpr int V = 16 / sizeof(T);
+  uint4 m[EDGE ? J : 1];
+  __device__ __forceinline__ explicit Inner(uint32_t valid) {
+    if constexpr (EDGE) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (sizeof(T) == 4) w[i] = valid >> (j * V + i) & 1 ? ~0u : 0u;
+          else w[i] = (valid >> (j * V + 2 * i) & 1 ? 0xffffu : 0u) | (valid >> (j * V + 2 * i + 1) & 1 ? 0xffff0000u : 0u);
+        }
+        m[j] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+  template <class Source>
+  __device__ __forceinline__ void get(const Source& rows, int a, f2 (&v)[V * J / 2]) const {
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      uint32_t w[4];
-      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                   : "r"(read + (a * J + j) * kPack)
-                   : "memory");
+      uint4 q = rows.word(a, j);
+      if constexpr (EDGE) {
+        q.x &= m[j].x;
+        q.y &= m[j].y;
+        q.z &= m[j].z;
+        q.w &= m[j].w;
+      }
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
       for (int i = 0; i < V; i += 2) {
         float x, y;
@@ -255,16 +299,10 @@ struct Ring {
         } else {
           unpack<T>(w[i / 2], x, y);
         }
-        if (EDGE) {
-          x = valid >> (j * V + i) & 1 ? x : 0.f;
-          y = valid >> (j * V + i + 1) & 1 ? y : 0.f;
-        }
         v[(j * V + i) / 2] = pack2(x, y);
       }
     }
   }
-  __device__ __forceinline__ void done() { read = read == mine + (kSlots - 1) * kSlot ? mine : read + kSlot; }
-  __device__ __forceinline__ void finish() const { asm volatile("cp.async.wait_all;" ::: "memory"); }
 };
 
 // A thread's packs of an output, row by row.
@@ -272,12 +310,13 @@ template <class T, int J, int TH, bool EDGE>
 struct Out {
   static constexpr int V = 16 / sizeof(T);
   char* p;                   // this lane's pack 0 in the current row; NULL: not wanted
-  long long row_step, pack_step;
+  long long row_step;
+  uint32_t pack_step;
   __device__ __forceinline__ Out(void* array, const NodeDesc& D, const Place<TH, EDGE>& at) {
     const long long first = (long long)at.n * D.dim + at.B.off + at.template elem<V>(0);
     p = array ? (char*)array + first * (int)sizeof(T) : nullptr;
     row_step = (long long)at.stride * D.dim * (int)sizeof(T);
-    pack_step = (long long)at.step * (int)sizeof(T);
+    pack_step = at.step * (uint32_t)sizeof(T);
   }
   __device__ __forceinline__ explicit operator bool() const { return p != nullptr; }
   __device__ __forceinline__ void put(const f2 (&v)[V * J / 2], uint32_t valid) const {
@@ -288,8 +327,8 @@ struct Out {
       for (int i = 0; i < V; i += 2) {
         const f2 q = v[(j * V + i) / 2];
         if constexpr (sizeof(T) == 4) {
-          w[i] = (uint32_t)q;
-          w[i + 1] = (uint32_t)(q >> 32);
+          w[i] = __float_as_uint(lo(q));
+          w[i + 1] = __float_as_uint(hi(q));
         } else {
           w[i / 2] = pack<T>(lo(q), hi(q));
         }
@@ -330,9 +369,17 @@ __device__ __forceinline__ uint32_t valid_bits(const P& at) {
 // where there is no vector, zeros outside the segment).
 __device__ __forceinline__ void expand(float* to, int n, const float* vec, const Channels& ch, int S, int shift,
                                        float missing) {
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int s = i - shift;
-    to[i] = s < 0 || s >= S ? 0.f : vec ? vec[ch.of(s)] : missing;
+  // eight loads on the way at a time: this is a CTA's first wait for memory
+  for (int i0 = threadIdx.x; i0 < n; i0 += 8 * blockDim.x) {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int s = i0 + k * (int)blockDim.x - shift;
+      v[k] = s < 0 || s >= S ? 0.f : vec ? vec[ch.of(s)] : missing;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (i0 + k * (int)blockDim.x < n) to[i0 + k * blockDim.x] = v[k];
   }
 }
 
@@ -433,7 +480,7 @@ __device__ __forceinline__ void shift_by(f2 (&v)[V * J / 2], float m, uint32_t v
 // Shared memory of a CTA: the ring (after the rows: the sums over them), vectors expanded per
 // element, the exchange between warps, keep bits.
 __host__ __device__ constexpr int rows_bytes(int elems, int arrays, int packs, bool sums, int threads) {
-  const int ring = ring_slots(16 * arrays * packs) * 16 * arrays * packs * threads, acc = sums ? threads * elems * 4 : 0;
+  const int ring = ring_slots(16 / (elems / packs), 16 * arrays * packs) * 16 * arrays * packs * threads, acc = sums ? threads * elems * 4 : 0;
   return ring > acc ? ring : acc;
 }
 // a vector's elements as far as any lane reads them
@@ -443,11 +490,17 @@ constexpr int mask_bytes(int elems, int threads) { return threads * elems / 4 + 
 
 extern __shared__ __align__(16) char g_smem[];
 
-#define TPC_NODE_KERNEL(TH, MIN) __global__ void __launch_bounds__(TH, (TH) == kThreads ? (MIN) : 1)
+enum Pass { PASS_FWD = NORM_FORWARD, PASS_BWD = NORM_BACKWARD, PASS_DBL = NORM_DOUBLE_BACKWARD };
+
+// CTAs of 256 threads that an SM is to hold (a bound on the registers).
+constexpr int min_ctas(Pass pass, int elems) { return pass == PASS_FWD && elems <= 8 ? 3 : 2; }
+
+#define TPC_NODE_KERNEL(TH, PASS, ELEMS) \
+  __global__ void __launch_bounds__(TH, (TH) == kThreads ? min_ctas(PASS, ELEMS) : 1)
 
 // Dropout (DROP) and norm (NORM) of x, either or both; with DROP the sum with the residual is z.
 template <class T, int J, int TH, bool EDGE, bool DROP, bool NORM>
-TPC_NODE_KERNEL(TH, 2)
+TPC_NODE_KERNEL(TH, PASS_FWD, 16 / sizeof(T) * J)
     k_fwd(const __grid_constant__ NodeDesc D, const __grid_constant__ RowMap M, const __grid_constant__ Drop drop,
           const __grid_constant__ NormArgs A, const uint32_t N) {
   constexpr int V = 16 / sizeof(T), E = V * J, P = E / 2, R = DROP ? 2 : 1;
@@ -459,9 +512,9 @@ TPC_NODE_KERNEL(TH, 2)
   const float inv = 1.f / (float)B.S;
   float* sw = reinterpret_cast<float*>(reinterpret_cast<char*>(part) + kPartBytes);
   float* sb = sw + (E << at.lg);
-  Ring<T, J, R, TH, EDGE> ring;
-  if constexpr (DROP) ring.start(g_smem, D, at, N, {A.x, A.residual});
-  else ring.start(g_smem, D, at, N, {A.x});
+  Ring<T, J, R, TH, EDGE> rows;
+  if constexpr (DROP) rows.start(g_smem, D, at, N, {A.x, A.residual});
+  else rows.start(g_smem, D, at, N, {A.x});
   if constexpr (NORM) {
     expand(sw, E << at.lg, A.weight ? A.weight + B.chan0 : nullptr, ch, B.S, at.shift, 1.f);
     expand(sb, E << at.lg, centred && A.bias ? A.bias + B.bias0 : nullptr, ch, B.S, at.shift, 0.f);
@@ -469,17 +522,23 @@ TPC_NODE_KERNEL(TH, 2)
   }
   Mask<V, J> mask(reinterpret_cast<unsigned char*>(NORM ? sb + (E << at.lg) : sw), at, D, drop);
   const uint32_t valid = valid_bits<V, J>(at);
+  const Inner<T, J, EDGE> inner(valid);
   Out<T, J, TH, EDGE> y(NORM ? A.y : nullptr, D, at), z(DROP ? A.z : nullptr, D, at);
+  f2 w[NORM ? P : 1], b[NORM ? P : 1];
+  if constexpr (NORM) {
+    lookup<V, J>(w, sw, at);
+    lookup<V, J>(b, sb, at);
+  }
   for (uint32_t n = at.n; at.more(n, N); n += at.stride) {
     const bool ok = n < N;
-    ring.next();
+    rows.next();
     f2 v[P];
-    ring.get(0, v, valid);
+    inner.get(rows, 0, v);
     if constexpr (DROP) {
       apply_mask(v, mask.bits(drop, at, ch, n, valid), drop.scale);
       if (A.residual) {
         f2 r[P];
-        ring.get(R - 1, r, valid);
+        inner.get(rows, R - 1, r);
 #pragma unroll
         for (int p = 0; p < P; ++p) v[p] = add2(v[p], r[p]);
       }
@@ -497,18 +556,15 @@ TPC_NODE_KERNEL(TH, 2)
       for (int p = 1; p < P; ++p) q2 = fma2(v[p], v[p], q2);
       float q[1] = {lo(q2) + hi(q2)};
       at.sum(q);
-      const f2 r = both(__frsqrt_rn(q[0] * inv + D.eps));
-      f2 w[P], b[P];
-      lookup<V, J>(w, sw, at);
-      lookup<V, J>(b, sb, at);
+      const f2 r = both(rsqrtf(q[0] * inv + D.eps));
 #pragma unroll
       for (int p = 0; p < P; ++p) v[p] = fma2(mul2(v[p], r), w[p], b[p]);
       if (ok) y.put(v, valid);
       y.next();
     }
-    ring.done();
+    rows.done();
   }
-  ring.finish();
+  rows.finish();
 }
 
 // Adds the lanes' sums over rows of a CTA and writes them per channel.
@@ -554,7 +610,7 @@ __device__ __forceinline__ float* sums_out(const RowMap& M, const NodeBlock& B, 
 }
 
 template <class T, int J, int TH, bool EDGE, bool DROP>
-TPC_NODE_KERNEL(TH, 2)
+TPC_NODE_KERNEL(TH, PASS_BWD, 16 / sizeof(T) * J)
     k_bwd(const __grid_constant__ NodeDesc D, const __grid_constant__ RowMap M, const __grid_constant__ Drop drop,
           const __grid_constant__ NormArgs A, const uint32_t N) {
   constexpr int V = 16 / sizeof(T), E = V * J, P = E / 2, R = DROP ? 3 : 2;
@@ -565,25 +621,26 @@ TPC_NODE_KERNEL(TH, 2)
   const bool centred = B.bias0 >= 0;
   const float inv = 1.f / (float)B.S;
   float* ws = reinterpret_cast<float*>(reinterpret_cast<char*>(part) + kPartBytes);
-  Ring<T, J, R, TH, EDGE> ring;
-  if constexpr (DROP) ring.start(g_smem, D, at, N, {A.x, A.grad_y, A.grad_z});
-  else ring.start(g_smem, D, at, N, {A.x, A.grad_y});
+  Ring<T, J, R, TH, EDGE> rows;
+  if constexpr (DROP) rows.start(g_smem, D, at, N, {A.x, A.grad_y, A.grad_z});
+  else rows.start(g_smem, D, at, N, {A.x, A.grad_y});
   expand(ws, E << at.lg, A.weight ? A.weight + B.chan0 : nullptr, ch, B.S, at.shift, 1.f);
   __syncthreads();
   Mask<V, J> mask(reinterpret_cast<unsigned char*>(ws + (E << at.lg)), at, D, drop);
   const uint32_t valid = valid_bits<V, J>(at);
+  const Inner<T, J, EDGE> inner(valid);
   f2 sw[P], sb[P];
 #pragma unroll
   for (int p = 0; p < P; ++p) sw[p] = sb[p] = 0;
   Out<T, J, TH, EDGE> gx(A.grad_x, D, at), gr(DROP ? A.grad_residual : nullptr, D, at);
   for (uint32_t n = at.n; at.more(n, N); n += at.stride) {
     const bool ok = n < N;
-    ring.next();
+    rows.next();
     f2 u[P], a[P];
-    ring.get(0, u, valid);
+    inner.get(rows, 0, u);
     {
       f2 w[P];
-      ring.get(1, a, valid);
+      inner.get(rows, 1, a);
       lookup<V, J>(w, ws, at);
       if (centred && ok) {
 #pragma unroll
@@ -606,10 +663,10 @@ TPC_NODE_KERNEL(TH, 2)
     }
     float q[2] = {lo(q0) + hi(q0), lo(q1) + hi(q1)};
     at.sum(q);
-    const float r = __frsqrt_rn(q[0] * inv + D.eps);
+    const float r = rsqrtf(q[0] * inv + D.eps);
     {
       f2 g[P];
-      ring.get(1, g, valid);   // read again instead of held: the registers carry the sums
+      inner.get(rows, 1, g);   // read again instead of held: the registers carry the sums
       const f2 r2 = both(r), mh = both(-(r * q[1] * inv));
 #pragma unroll
       for (int p = 0; p < P; ++p) {
@@ -621,7 +678,7 @@ TPC_NODE_KERNEL(TH, 2)
     if constexpr (DROP) {
       if (A.grad_z) {
         f2 t[P];
-        ring.get(R - 1, t, valid);
+        inner.get(rows, R - 1, t);
 #pragma unroll
         for (int p = 0; p < P; ++p) u[p] = add2(u[p], t[p]);
       }
@@ -631,9 +688,10 @@ TPC_NODE_KERNEL(TH, 2)
     }
     if (gx && ok) gx.put(u, valid);
     gx.next();
-    ring.done();
+    rows.done();
   }
-  ring.finish();
+  rows.finish();
+  cudaTriggerProgrammaticLaunchCompletion();
   float* smem = reinterpret_cast<float*>(g_smem);
   if (float* out = sums_out(M, B, at.k, A.partial, A.grad_weight, B.chan0, false))
     write_sums<V, J>(sw, smem, out, at, ch);
@@ -643,7 +701,7 @@ TPC_NODE_KERNEL(TH, 2)
 }
 
 template <class T, int J, int TH, bool EDGE>
-TPC_NODE_KERNEL(TH, 2)
+TPC_NODE_KERNEL(TH, PASS_DBL, 16 / sizeof(T) * J)
     k_dbl(const __grid_constant__ NodeDesc D, const __grid_constant__ RowMap M, const __grid_constant__ NormArgs A,
           const uint32_t N) {
   constexpr int V = 16 / sizeof(T), E = V * J, P = E / 2;
@@ -655,30 +713,31 @@ TPC_NODE_KERNEL(TH, 2)
   const float inv = 1.f / (float)B.S;
   float* ws = reinterpret_cast<float*>(reinterpret_cast<char*>(part) + kPartBytes);
   float *ts = ws + (E << at.lg), *bs = ts + (E << at.lg);
-  Ring<T, J, 3, TH, EDGE> ring;
-  ring.start(g_smem, D, at, N, {A.x, A.grad_y, A.gg_x});
+  Ring<T, J, 3, TH, EDGE> rows;
+  rows.start(g_smem, D, at, N, {A.x, A.grad_y, A.gg_x});
   expand(ws, E << at.lg, A.weight ? A.weight + B.chan0 : nullptr, ch, B.S, at.shift, 1.f);
   expand(ts, E << at.lg, A.gg_weight ? A.gg_weight + B.chan0 : nullptr, ch, B.S, at.shift, 0.f);
   expand(bs, E << at.lg, centred && A.gg_bias ? A.gg_bias + B.bias0 : nullptr, ch, B.S, at.shift, 0.f);
   __syncthreads();
   const uint32_t valid = valid_bits<V, J>(at);
+  const Inner<T, J, EDGE> inner(valid);
   f2 sw[P];
 #pragma unroll
   for (int p = 0; p < P; ++p) sw[p] = 0;
   Out<T, J, TH, EDGE> gx(A.grad_x, D, at), gg(A.grad_grad_y, D, at);
   for (uint32_t n = at.n; at.more(n, N); n += at.stride) {
     const bool ok = n < N;
-    ring.next();
+    rows.next();
     // u, p, a = weight g, e = gg_weight g; less their means in a 0e block
     f2 u[P], pt[P], a[P], e[P], w[P], t[P];
-    ring.get(0, u, valid);
+    inner.get(rows, 0, u);
     if (A.gg_x) {
-      ring.get(2, pt, valid);
+      inner.get(rows, 2, pt);
     } else {
 #pragma unroll
       for (int p = 0; p < P; ++p) pt[p] = 0;
     }
-    ring.get(1, a, valid);
+    inner.get(rows, 1, a);
     lookup<V, J>(w, ws, at);
     lookup<V, J>(t, ts, at);
 #pragma unroll
@@ -709,13 +768,13 @@ TPC_NODE_KERNEL(TH, 2)
 #pragma unroll
     for (int k = 0; k < 5; ++k) q[k] = lo(q2[k]) + hi(q2[k]);
     at.sum(q);
-    const float r = __frsqrt_rn(q[0] * inv + D.eps);
+    const float r = rsqrtf(q[0] * inv + D.eps);
     const float mp = r * q[1] * inv, ma = r * q[2] * inv, mpa = q[3] * inv, me = r * q[4] * inv;
     // grad_x = h (r^2 (3 mp ma - mpa) - r me) - r^2 ma p - r^2 mp a + r e,  k = r (p - h mp)
     const f2 r2 = both(r), c_h = both(r * r * (3.f * mp * ma - mpa) - r * me), c_p = both(-(r * r * ma)),
              c_a = both(-(r * r * mp)), nmp = both(-mp);
     f2 g[P], b[P];
-    ring.get(1, g, valid);
+    inner.get(rows, 1, g);
     lookup<V, J>(w, ws, at);
     lookup<V, J>(t, ts, at);
     lookup<V, J>(b, bs, at);
@@ -730,11 +789,98 @@ TPC_NODE_KERNEL(TH, 2)
     if (gg && ok) gg.put(e, valid);
     gx.next();
     gg.next();
-    ring.done();
+    rows.done();
   }
-  ring.finish();
+  rows.finish();
+  cudaTriggerProgrammaticLaunchCompletion();
   if (float* out = sums_out(M, B, at.k, A.partial, A.grad_weight, B.chan0, false))
     write_sums<V, J>(sw, reinterpret_cast<float*>(g_smem), out, at, ch);
+}
+
+// ---- dropout alone in 16 bits, blocks whose channels come in whole packs: a thread owns V channels of
+// a row ----
+//
+// Bound by instructions (the generator's) more than by HBM.  With all 2l+1 components of its channels
+// in one thread, a counter is drawn once for them and needs no exchange between lanes: 16384 x 1152
+// bf16 17 us (68 % of the copy bandwidth), 27 us by k_fwd.  Four CTAs an SM and one row a step (two
+// for scalars) measured best.  In float32 k_fwd's ring is faster (50000 x 592 with residual: 57 us, 65
+// us here).
+
+template <class T, int DC, bool MUL_IR>
+__device__ __forceinline__ void drop_block(const NodeDesc& D, const NodeBlock& B, const Drop& drop, const T* x,
+                                           const T* res, T* out, uint32_t N, uint32_t cta, uint32_t ctas) {
+  constexpr int V = 16 / sizeof(T), U = DC == 1 ? 2 : 1;
+  const uint32_t packs = B.C / V, lanes = packs < kThreads ? packs : kThreads, rows = kThreads / lanes;
+  const uint32_t slot = threadIdx.x / lanes, lane = threadIdx.x - slot * lanes;
+  if (slot >= rows) return;
+  const uint64_t off = drop.mode == 1 ? drop_offset(drop) : 0;
+  const int step = MUL_IR ? V : B.C;  // elements between a thread's packs
+  for (uint32_t n0 = cta * rows * U + slot; n0 < N; n0 += ctas * rows * U)
+    for (uint32_t q = lane; q < packs; q += lanes) {
+      const uint32_t first = B.off + q * (MUL_IR ? V * DC : V);
+      uint4 a[U][DC], b[U][DC];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t n = n0 + u * rows;
+        if (n >= N) break;
+        const long long at = (long long)n * D.dim + first;
+#pragma unroll
+        for (int k = 0; k < DC; ++k) {
+          a[u][k] = *reinterpret_cast<const uint4*>(x + at + k * step);
+          if (res) b[u][k] = *reinterpret_cast<const uint4*>(res + at + k * step);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t n = n0 + u * rows;
+        if (n >= N) break;
+        uint32_t keep = drop.mode == 0 ? ~0u : 0u;
+        if (drop.mode == 1) {
+#pragma unroll
+          for (int g = 0; g < V / 4; ++g) {
+            const uint4 w = drop_words(drop, off, B.grp0 + q * (V / 4) + g, n);
+            keep |= ((w.x >= drop.threshold ? 1u : 0u) | (w.y >= drop.threshold ? 2u : 0u) |
+                     (w.z >= drop.threshold ? 4u : 0u) | (w.w >= drop.threshold ? 8u : 0u))
+                    << (4 * g);
+          }
+        }
+        T* to = out + (long long)n * D.dim + first;
+#pragma unroll
+        for (int k = 0; k < DC; ++k) {
+          const uint32_t wa[4] = {a[u][k].x, a[u][k].y, a[u][k].z, a[u][k].w};
+          const uint32_t wb[4] = {b[u][k].x, b[u][k].y, b[u][k].z, b[u][k].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < V; i += 2) {
+            const int c0 = MUL_IR ? (k * V + i) / DC : i, c1 = MUL_IR ? (k * V + i + 1) / DC : i + 1;
+            float v0, v1, r0 = 0.f, r1 = 0.f;
+            unpack<T>(wa[i / 2], v0, v1);
+            if (res) unpack<T>(wb[i / 2], r0, r1);
+            v0 = keep >> c0 & 1 ? __fmul_rn(v0, drop.scale) : 0.f;
+            v1 = keep >> c1 & 1 ? __fmul_rn(v1, drop.scale) : 0.f;
+            if (res) v0 += r0, v1 += r1;
+            o[i / 2] = pack<T>(v0, v1);
+          }
+          *reinterpret_cast<uint4*>(to + k * step) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+    }
+}
+
+template <class T, bool MUL_IR>
+__global__ void __launch_bounds__(kThreads, kDropCtas)
+    k_drop(const __grid_constant__ NodeDesc D, const __grid_constant__ RowMap M, const __grid_constant__ Drop drop,
+           const T* x, const T* res, T* out, const uint32_t N) {
+  int k = 0;
+  while (k + 1 < M.n && (int)blockIdx.x >= M.cta0[k + 1]) ++k;
+  const NodeBlock& B = D.b[M.blk[k]];
+  const uint32_t cta = blockIdx.x - M.cta0[k], ctas = M.cta0[k + 1] - M.cta0[k];
+  switch (B.d) {
+    case 1: return drop_block<T, 1, false>(D, B, drop, x, res, out, N, cta, ctas);
+    case 3: return drop_block<T, 3, MUL_IR>(D, B, drop, x, res, out, N, cta, ctas);
+    case 5: return drop_block<T, 5, MUL_IR>(D, B, drop, x, res, out, N, cta, ctas);
+    default: return drop_block<T, 7, MUL_IR>(D, B, drop, x, res, out, N, cta, ctas);
+  }
 }
 
 // ---- any width: one CTA per segment, read again for each sum; a thread owns whole channels ----
@@ -802,7 +948,7 @@ __global__ void __launch_bounds__(kThreads)
         q[0] += u * u;
       });
       cta_sum(q, flip);
-      r = __frsqrt_rn(q[0] * inv + D.eps);
+      r = rsqrtf(q[0] * inv + D.eps);
     }
     each(B, D.mul_ir, [&](int c, int s) {
       const float v = value(c, s);
@@ -845,7 +991,7 @@ __global__ void __launch_bounds__(kThreads)
       q[1] += u * (a(c, s) - ma);
     });
     cta_sum(q, flip);
-    const float r = __frsqrt_rn(q[0] * inv + D.eps), mh = r * q[1] * inv;
+    const float r = rsqrtf(q[0] * inv + D.eps), mh = r * q[1] * inv;
     for (int c = threadIdx.x; c < B.C; c += kThreads) {
       float sw = 0.f, sb = 0.f;
       for (int k = 0; k < B.d; ++k) {
@@ -906,7 +1052,7 @@ __global__ void __launch_bounds__(kThreads)
       q[4] += u * (tangent(c) * gv - mw);
     });
     cta_sum(q, flip);
-    const float r = __frsqrt_rn(q[0] * inv + D.eps);
+    const float r = rsqrtf(q[0] * inv + D.eps);
     const float P = r * q[1] * inv, Q = r * q[2] * inv, R = q[3] * inv, W = r * q[4] * inv;
     for (int c = threadIdx.x; c < B.C; c += kThreads) {
       const float w = weight(c), t = tangent(c), b = centred && A.gg_bias ? A.gg_bias[B.bias0 + c] : 0.f;
@@ -942,6 +1088,7 @@ __global__ void __launch_bounds__(32 * kShares)
   float* out = bias ? grad_bias : grad_weight;
   bool wanted = out && i < D.channels + D.biases;
   float v = 0.f;
+  cudaGridDependencySynchronize();  // the partial sums are complete
   if (wanted) {
     int k = 0;
     for (; k < M.n; ++k) {
@@ -972,7 +1119,6 @@ __global__ void __launch_bounds__(32 * kShares)
 
 // ---- launch plan ----
 
-enum Pass { PASS_FWD = NORM_FORWARD, PASS_BWD = NORM_BACKWARD, PASS_DBL = NORM_DOUBLE_BACKWARD };
 enum Kind { KIND_GROUP, KIND_WIDE, KIND_ANY };  // 256 threads, one group of 512, any width
 
 struct Launch {
@@ -1049,10 +1195,14 @@ LaunchPlan plan_launches(const Shape& sh, const NodeDesc& D, long long N) {
       resident = sums ? kAnyParts : kSms * 8;
       for (int k = 0; k < M.n; ++k) M.lg[k] = log2_lanes(kThreads, 1);
     } else {
-      // fewest lane-packs per row; a segment's lanes are a power of two
-      const int lg_max = log2_lanes(L.threads, 1);
+      // Fewest lane-packs per row (a segment's lanes are a power of two); of equal ones the most
+      // packs per lane, but 12 elements in the passes with sums and dropout alone (fused backward 50000 x 592 f32: 104
+      // us, 112 us with 16), and 8 off the boundary, where each element costs more instructions
+      // (backward 50000 x 145 f32: 30 us, 32 us with 12; f16 mul_ir: 35 us, 41 us with 16).
+      const int lg_max = log2_lanes(L.threads, 1), few = P.edge ? 8 : sums || !sh.norm ? 12 : 16;
       long long best = -1;
       for (int j = kd == KIND_WIDE ? jmax : 1; j <= jmax; ++j) {
+        if (P.edge && V * j > few && best >= 0) break;
         long long cost = 0;
         bool fits = true;
         for (int k = 0; k < M.n; ++k) {
@@ -1060,7 +1210,9 @@ LaunchPlan plan_launches(const Shape& sh, const NodeDesc& D, long long N) {
           fits = fits && lg <= lg_max;
           cost += (long long)j << lg;
         }
-        if (fits && (best < 0 || cost <= best)) {
+        int lanes = 0;
+        for (int k = 0; k < M.n; ++k) lanes = std::max(lanes, 1 << log2_lanes(D.b[M.blk[k]].S + pad, V * j));
+        if (fits && (best < 0 || cost < best || (cost == best && (V * j <= few || lanes > 32)))) {
           best = cost;
           L.J = j;
         }
@@ -1071,7 +1223,7 @@ LaunchPlan plan_launches(const Shape& sh, const NodeDesc& D, long long N) {
         widest = M.lg[k] > widest ? M.lg[k] : widest;
       }
       L.smem = sh.smem(L.J, L.threads, widest);
-      resident = kSms * ctas_per_sm(kd == KIND_WIDE ? 1 : 2, L.smem);
+      resident = kSms * ctas_per_sm(kd == KIND_WIDE ? 1 : min_ctas(sh.pass, V * L.J), L.smem);
     }
     // Steps of a CTA: as few as let all CTAs run at a time.  Few rows: one CTA per block, whose sums
     // need no second launch.
@@ -1190,8 +1342,46 @@ void run_any(const Call& c, const Launch& L) {
   }
 }
 
+// Dropout alone where every block's channels come in whole packs; false: not such rows.
+template <class T>
+bool run_drop(const Call& c) {
+  constexpr int V = 16 / sizeof(T);
+  for (int b = 0; b < c.D.n_blocks; ++b)
+    if (c.D.b[b].C % V != 0) return false;
+  RowMap M{};
+  M.n = c.D.n_blocks;
+  for (int b = 0; b < M.n; ++b) {
+    const NodeBlock& B = c.D.b[b];
+    M.blk[b] = b;
+    const long long packs = B.C / V, rows = packs < kThreads ? kThreads / packs : 1;
+    const long long most = (c.N + rows - 1) / rows, share = (long long)kSms * kDropCtas * B.S / c.D.dim;
+    M.cta0[b + 1] = M.cta0[b] + (int)(share < 1 ? 1 : share > most ? most : share);
+  }
+  const dim3 grid(M.cta0[M.n]), block(kThreads);
+  const T *x = (const T*)c.A.x, *res = (const T*)c.A.residual;
+  if (c.D.mul_ir) k_drop<T, true><<<grid, block, 0, c.s>>>(c.D, M, c.d, x, res, (T*)c.A.z, c.N);
+  else k_drop<T, false><<<grid, block, 0, c.s>>>(c.D, M, c.d, x, res, (T*)c.A.z, c.N);
+  return true;
+}
+
+// The reduction is set up while the rows' kernel drains (programmatic launch).
+cudaError_t run_reduce(const Call& c, const PartMap& parts) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((c.D.channels + c.D.biases + 31) / 32);
+  cfg.blockDim = dim3(32 * kShares);
+  cfg.stream = c.s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_norm_reduce, c.D, parts, (const float*)c.A.partial, c.A.grad_weight, c.A.grad_bias);
+}
+
 template <class T>
 cudaError_t run_node(const Call& c) {
+  if constexpr (sizeof(T) == 2)
+    if (!c.norm && run_drop<T>(c)) return cudaGetLastError();
   const LaunchPlan P = plan_launches(Shape{c.pass, c.drop, c.norm, sizeof(T), 16 / sizeof(T)}, c.D, c.N);
   for (int i = 0; i < P.n; ++i) {
     const Launch& L = P.l[i];
@@ -1199,9 +1389,10 @@ cudaError_t run_node(const Call& c) {
     else if (P.edge) run_packs<T, true>(c, L);
     else run_packs<T, false>(c, L);
   }
-  if (c.A.partial && P.parts.n)
-    k_norm_reduce<<<(c.D.channels + c.D.biases + 31) / 32, 32 * kShares, 0, c.s>>>(c.D, P.parts, c.A.partial,
-                                                                                 c.A.grad_weight, c.A.grad_bias);
+  if (c.A.partial && P.parts.n) {
+    const cudaError_t e = run_reduce(c, P.parts);
+    if (e != cudaSuccess) return e;
+  }
   return cudaGetLastError();
 }
 

@@ -15,19 +15,16 @@ template <> __device__ __forceinline__ float from_f32<float>(float v) { return v
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
-// Philox4x32-10: ten rounds of two 32 x 32 -> 64 products on a 128-bit counter, the key
-// advanced by fixed odd increments (Salmon et al. 2011, section 4.3).
-__device__ __forceinline__ uint4 philox10(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t k0,
-                                          uint32_t k1) {
+// Philox4x32-10: ten rounds of two 32 x 32 -> 64 products on a 128-bit counter (Salmon et al. 2011,
+// section 4.3); the rounds' keys come with the call.
+__device__ __forceinline__ uint4 philox10(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, const Drop& D) {
 #pragma unroll
   for (int i = 0; i < 10; ++i) {
     const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
-    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+    c0 = (uint32_t)(b >> 32) ^ c1 ^ D.key[i][0];
     c1 = (uint32_t)b;
-    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+    c2 = (uint32_t)(a >> 32) ^ c3 ^ D.key[i][1];
     c3 = (uint32_t)a;
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
   }
   return make_uint4(c0, c1, c2, c3);
 }
@@ -43,7 +40,7 @@ __device__ __forceinline__ uint64_t drop_offset(const Drop& D) {
 
 // Words of a row's channel group.
 __device__ __forceinline__ uint4 drop_words(const Drop& D, uint64_t off, uint32_t group, uint32_t row) {
-  return philox10(group, row, (uint32_t)off, (uint32_t)(off >> 32), D.k0, D.k1);
+  return philox10(group, row, (uint32_t)off, (uint32_t)(off >> 32), D);
 }
 
 // kept ? v * scale : 0 for one channel, drawing its group's words

@@ -25,7 +25,7 @@ struct NodeDesc {
 
 // Dropout of one call as the kernels see it.
 struct Drop {
-  uint32_t k0, k1;        // key: low and high word of the seed
+  uint32_t key[10][2];    // the seed's words, and what each round makes of them
   uint64_t offset;
   const long long* step;  // device, added to offset; may be NULL
   uint32_t threshold;     // dropped iff word < threshold

@@ -64,8 +64,10 @@ bool rows_ok(const tpconv_node_plan* P, int64_t N) { return P && N >= 0 && N < 0
 tpconv_status make_drop(const tpconv_dropout_spec* spec, Drop& d) {
   if (!spec || !(spec->p >= 0.0 && spec->p <= 1.0)) return TPCONV_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(spec->step) & 7u) != 0) return TPCONV_ERR_MISALIGNED;
-  d.k0 = (uint32_t)spec->seed;
-  d.k1 = (uint32_t)(spec->seed >> 32);
+  for (uint32_t i = 0; i < 10; ++i) {  // each round advances the key by fixed odd increments
+    d.key[i][0] = (uint32_t)spec->seed + i * 0x9E3779B9u;
+    d.key[i][1] = (uint32_t)(spec->seed >> 32) + i * 0xBB67AE85u;
+  }
   d.offset = spec->offset;
   d.step = reinterpret_cast<const long long*>(spec->step);
   const double t = std::floor(spec->p * 4294967296.0 + 0.5);
