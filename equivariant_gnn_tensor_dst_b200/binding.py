@@ -210,10 +210,9 @@ def _stream(stream):
 
 def _raw_stream(stream, device):
     """The stream handle as an integer (building a torch Stream object costs several microseconds)."""
-    import torch
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return _torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _need(t, dtype, name):
@@ -409,13 +408,18 @@ def tpconv_gather_rows(a, perm, stream=None):
 # node-feature operators (include/tpconv_node.h)
 # ---------------------------------------------------------------------------
 
+_torch = None   # torch, once a NodePlan exists (an import statement in every call costs)
+
+
 class NodePlan:
     """tpconv_node_plan_create / _destroy: rows of an irreps string in a storage type
     (torch.float32, bfloat16 or float16), the norm's eps and the layout ("ir_mul" or
     "mul_ir", or the LAYOUT_ constants)."""
 
     def __init__(self, irreps, dtype=None, eps=1e-5, layout=LAYOUT_IR_MUL):
+        global _torch
         import torch
+        _torch = torch
         dtype = torch.float32 if dtype is None else dtype
         codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
         if dtype not in codes:
@@ -509,43 +513,53 @@ def _node_bad(t, name, dtype, shape, device):
     raise ValueError(f"{name} must be on {device}")
 
 
-def _node_ptrs(plan, x, name, rows, params):
-    """Checks node arrays (``rows``: (tensor or None, name), of x's shape, in the plan's type) and
-    channel vectors (``params``: (tensor or None, length, name), float32), all contiguous and on
-    x's device; returns their addresses (0 for None) in that order, x first."""
-    import torch
-    dtype, shape, device = plan.dtype, x.shape, x.device
-    if not (x.is_cuda and x.dtype is dtype and x.is_contiguous() and len(shape) == 2 and shape[1] == plan.dim):
-        _need(x, dtype, name)
+def _node_x(plan, x, name):
+    """Checks the array that sets a call's rows and device; its address."""
+    shape = x.shape
+    if not (x.is_cuda and x.dtype is plan.dtype and x.is_contiguous() and len(shape) == 2 and shape[1] == plan.dim):
+        _need(x, plan.dtype, name)
         raise ValueError(f"{name} must be [rows, {plan.dim}], not {list(shape)}")
-    ptrs = [x.data_ptr()]
-    for t, what in rows:
-        if t is None:
-            ptrs.append(0)
-            continue
-        if not (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
-            _node_bad(t, what, dtype, shape, device)
-        ptrs.append(t.data_ptr())
-    for t, n, what in params:
-        if t is None:
-            ptrs.append(0)
-            continue
-        if not (t.dtype is torch.float32 and t.numel() == n and t.device == device and t.is_contiguous()):
-            _node_bad(t, what, torch.float32, (n,), device)
-        ptrs.append(t.data_ptr())
-    return ptrs
+    return x.data_ptr()
 
 
-def _channel_sums(weight, n, device):
-    import torch
-    return torch.empty_like(weight) if weight is not None else torch.empty(n, dtype=torch.float32, device=device)
+def _node_row(t, name, x):
+    """Address of a node array like x (0: None)."""
+    if t is None:
+        return 0
+    if not (t.dtype is x.dtype and t.shape == x.shape and t.device == x.device and t.is_contiguous()):
+        _node_bad(t, name, x.dtype, x.shape, x.device)
+    return t.data_ptr()
+
+
+def _node_vec(t, n, name, x):
+    """Address of a float32 channel vector of n values on x's device (0: None)."""
+    if t is None:
+        return 0
+    if not (t.dtype is _torch.float32 and t.numel() == n and t.device == x.device and t.is_contiguous()):
+        _node_bad(t, name, _torch.float32, (n,), x.device)
+    return t.data_ptr()
+
+
+def _node_new(like, need):
+    """A new array like another and its address."""
+    if not need:
+        return None, 0
+    t = _torch.empty_like(like)
+    return t, t.data_ptr()
+
+
+def _node_sums(like, n, need, device):
+    """A new channel vector (like another, where there is one) and its address."""
+    if not need:
+        return None, 0
+    t = _torch.empty_like(like) if like is not None else _torch.empty(n, dtype=_torch.float32, device=device)
+    return t, t.data_ptr()
 
 
 def _node_call(device, name, stream, *args):
     """One library call on the tensors' device and the given (or that device's current) stream."""
-    import torch
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
+    if device.index != _torch.cuda.current_device():
+        with _torch.cuda.device(device):
             return _node_call(device, name, stream, *args)
     status = getattr(_lib, name)(*args, _raw_stream(stream, device))
     if status:
@@ -563,105 +577,101 @@ def _node_ws(plan, N, ws, device):
 
 def tpconv_norm_forward(plan, x, weight=None, bias=None, out=None, stream=None):
     """Irreps layer norm of node rows x [N, dim]; weight [channels], bias [biases] float32."""
-    import torch
-    if out is None:
-        out = torch.empty_like(x)
-    px, po, pw, pb = _node_ptrs(plan, x, "x", ((out, "out"),),
-                                ((weight, plan.channels, "weight"), (bias, plan.biases, "bias")))
-    _node_call(x.device, "tpconv_norm_forward", stream, plan.handle, x.shape[0], px, pw, pb, po)
+    px = _node_x(plan, x, "x")
+    pw, pb = _node_vec(weight, plan.channels, "weight", x), _node_vec(bias, plan.biases, "bias", x)
+    out, po = _node_new(x, True) if out is None else (out, _node_row(out, "out", x))
+    _node_call(x.device, "tpconv_norm_forward", stream, plan._h, x.shape[0], px, pw, pb, po)
     return out
 
 
 def tpconv_norm_backward(plan, x, weight, grad_y, need_x=True, need_weight=True, need_bias=True, ws=None,
                          outputs=None, stream=None):
     """Returns (grad_x [N, dim], grad_weight [channels], grad_bias [biases])."""
-    import torch
-    dev, N = x.device, x.shape[0]
+    dev, N, C, Cb = x.device, x.shape[0], plan.channels, plan.biases
+    px, pg, pw = _node_x(plan, x, "x"), _node_row(grad_y, "grad_y", x), _node_vec(weight, C, "weight", x)
     if outputs is None:
-        gx = torch.empty_like(x) if need_x else None
-        gw = _channel_sums(weight, plan.channels, dev) if need_weight else None
-        gb = torch.empty(plan.biases, dtype=torch.float32, device=dev) if need_bias else None
+        gx, pgx = _node_new(x, need_x)
+        gw, pgw = _node_sums(weight, C, need_weight, dev)
+        gb, pgb = _node_sums(None, Cb, need_bias, dev)
     else:
         gx, gw, gb = outputs
-    px, pg, pgx, pw, pgw, pgb = _node_ptrs(
-        plan, x, "x", ((grad_y, "grad_y"), (gx, "grad_x")),
-        ((weight, plan.channels, "weight"), (gw, plan.channels, "grad_weight"), (gb, plan.biases, "grad_bias")))
+        pgx = _node_row(gx, "grad_x", x)
+        pgw, pgb = _node_vec(gw, C, "grad_weight", x), _node_vec(gb, Cb, "grad_bias", x)
     ws, pws, nws = _node_ws(plan, N, ws, dev)
-    _node_call(dev, "tpconv_norm_backward", stream, plan.handle, N, px, pw, pg, pgx, pgw, pgb, pws, nws)
+    _node_call(dev, "tpconv_norm_backward", stream, plan._h, N, px, pw, pg, pgx, pgw, pgb, pws, nws)
     return gx, gw, gb
 
 
 def tpconv_norm_double_backward(plan, x, weight, grad_y, gg_x=None, gg_weight=None, gg_bias=None, need_x=True,
                                 need_weight=True, need_grad_y=True, ws=None, outputs=None, stream=None):
     """Returns (grad_x [N, dim], grad_weight [channels], grad_grad_y [N, dim])."""
-    import torch
-    dev, N = x.device, x.shape[0]
+    dev, N, C = x.device, x.shape[0], plan.channels
+    px, pg, pp = _node_x(plan, x, "x"), _node_row(grad_y, "grad_y", x), _node_row(gg_x, "gg_x", x)
+    pw, pt = _node_vec(weight, C, "weight", x), _node_vec(gg_weight, C, "gg_weight", x)
+    ptb = _node_vec(gg_bias, plan.biases, "gg_bias", x)
     if outputs is None:
-        gx = torch.empty_like(x) if need_x else None
-        gw = _channel_sums(weight, plan.channels, dev) if need_weight else None
-        gg = torch.empty_like(x) if need_grad_y else None
+        gx, pgx = _node_new(x, need_x)
+        gw, pgw = _node_sums(weight, C, need_weight, dev)
+        gg, pgg = _node_new(x, need_grad_y)
     else:
         gx, gw, gg = outputs
-    px, pg, pp, pgx, pgg, pw, pt, ptb, pgw = _node_ptrs(
-        plan, x, "x", ((grad_y, "grad_y"), (gg_x, "gg_x"), (gx, "grad_x"), (gg, "grad_grad_y")),
-        ((weight, plan.channels, "weight"), (gg_weight, plan.channels, "gg_weight"), (gg_bias, plan.biases, "gg_bias"),
-         (gw, plan.channels, "grad_weight")))
+        pgx, pgg = _node_row(gx, "grad_x", x), _node_row(gg, "grad_grad_y", x)
+        pgw = _node_vec(gw, C, "grad_weight", x)
     ws, pws, nws = _node_ws(plan, N, ws, dev)
-    _node_call(dev, "tpconv_norm_double_backward", stream, plan.handle, N, px, pw, pg, pp, pt, ptb, pgx, pgw, pgg,
-               pws, nws)
+    _node_call(dev, "tpconv_norm_double_backward", stream, plan._h, N, px, pw, pg, pp, pt, ptb, pgx, pgw, pgg, pws,
+               nws)
     return gx, gw, gg
 
 
 def tpconv_dropout_forward(plan, x, dropout, residual=None, out=None, stream=None):
     """residual + dropout(x); ``dropout`` is a Dropout.  out may be x or residual (in place)."""
-    import torch
-    if out is None:
-        out = torch.empty_like(x)
-    px, pr, po = _node_ptrs(plan, x, "x", ((residual, "residual"), (out, "out")), ())
-    _node_call(x.device, "tpconv_dropout_forward", stream, plan.handle, x.shape[0], px, pr, dropout.spec(x.device), po)
+    px, pr = _node_x(plan, x, "x"), _node_row(residual, "residual", x)
+    out, po = _node_new(x, True) if out is None else (out, _node_row(out, "out", x))
+    _node_call(x.device, "tpconv_dropout_forward", stream, plan._h, x.shape[0], px, pr, dropout.spec(x.device), po)
     return out
 
 
 def tpconv_dropout_backward(plan, grad_out, dropout, out=None, stream=None):
     """grad_x of tpconv_dropout_forward (the residual's gradient is grad_out itself)."""
-    import torch
-    if out is None:
-        out = torch.empty_like(grad_out)
-    pg, po = _node_ptrs(plan, grad_out, "grad_out", ((out, "out"),), ())
-    _node_call(grad_out.device, "tpconv_dropout_backward", stream, plan.handle, grad_out.shape[0], pg,
+    pg = _node_x(plan, grad_out, "grad_out")
+    out, po = _node_new(grad_out, True) if out is None else (out, _node_row(out, "out", grad_out))
+    _node_call(grad_out.device, "tpconv_dropout_backward", stream, plan._h, grad_out.shape[0], pg,
                dropout.spec(grad_out.device), po)
     return out
 
 
 def tpconv_dropout_norm_forward(plan, x, dropout, residual=None, weight=None, bias=None, outputs=None, stream=None):
     """Returns (z, y): z = residual + dropout(x), y = norm(z)."""
-    import torch
-    z, y = (torch.empty_like(x), torch.empty_like(x)) if outputs is None else outputs
-    px, pr, pz, py, pw, pb = _node_ptrs(plan, x, "x", ((residual, "residual"), (z, "z"), (y, "y")),
-                                        ((weight, plan.channels, "weight"), (bias, plan.biases, "bias")))
-    _node_call(x.device, "tpconv_dropout_norm_forward", stream, plan.handle, x.shape[0], px, pr,
-               dropout.spec(x.device), pw, pb, pz, py)
+    px, pr = _node_x(plan, x, "x"), _node_row(residual, "residual", x)
+    pw, pb = _node_vec(weight, plan.channels, "weight", x), _node_vec(bias, plan.biases, "bias", x)
+    if outputs is None:
+        (z, pz), (y, py) = _node_new(x, True), _node_new(x, True)
+    else:
+        z, y = outputs
+        pz, py = _node_row(z, "z", x), _node_row(y, "y", x)
+    _node_call(x.device, "tpconv_dropout_norm_forward", stream, plan._h, x.shape[0], px, pr, dropout.spec(x.device),
+               pw, pb, pz, py)
     return z, y
 
 
 def tpconv_dropout_norm_backward(plan, z, weight, grad_y, dropout, grad_z=None, need_x=True, need_residual=True,
                                  need_weight=True, need_bias=True, ws=None, outputs=None, stream=None):
     """Returns (grad_x, grad_residual, grad_weight, grad_bias) from the stored z."""
-    import torch
-    dev, N = z.device, z.shape[0]
+    dev, N, C, Cb = z.device, z.shape[0], plan.channels, plan.biases
+    pz, pg, pgz = _node_x(plan, z, "z"), _node_row(grad_y, "grad_y", z), _node_row(grad_z, "grad_z", z)
+    pw = _node_vec(weight, C, "weight", z)
     if outputs is None:
-        gx = torch.empty_like(z) if need_x else None
-        gr = torch.empty_like(z) if need_residual else None
-        gw = _channel_sums(weight, plan.channels, dev) if need_weight else None
-        gb = torch.empty(plan.biases, dtype=torch.float32, device=dev) if need_bias else None
+        gx, pgx = _node_new(z, need_x)
+        gr, pgr = _node_new(z, need_residual)
+        gw, pgw = _node_sums(weight, C, need_weight, dev)
+        gb, pgb = _node_sums(None, Cb, need_bias, dev)
     else:
         gx, gr, gw, gb = outputs
-    pz, pg, pgz, pgx, pgr, pw, pgw, pgb = _node_ptrs(
-        plan, z, "z", ((grad_y, "grad_y"), (grad_z, "grad_z"), (gx, "grad_x"), (gr, "grad_residual")),
-        ((weight, plan.channels, "weight"), (gw, plan.channels, "grad_weight"), (gb, plan.biases, "grad_bias")))
+        pgx, pgr = _node_row(gx, "grad_x", z), _node_row(gr, "grad_residual", z)
+        pgw, pgb = _node_vec(gw, C, "grad_weight", z), _node_vec(gb, Cb, "grad_bias", z)
     ws, pws, nws = _node_ws(plan, N, ws, dev)
-    _node_call(dev, "tpconv_dropout_norm_backward", stream, plan.handle, N, pz, pw, pg, pgz, dropout.spec(dev), pgx,
-               pgr, pgw, pgb, pws, nws)
+    _node_call(dev, "tpconv_dropout_norm_backward", stream, plan._h, N, pz, pw, pg, pgz, dropout.spec(dev), pgx, pgr,
+               pgw, pgb, pws, nws)
     return gx, gr, gw, gb
 
 

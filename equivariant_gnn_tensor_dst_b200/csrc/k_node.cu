@@ -31,7 +31,7 @@ namespace tpc {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWide = 512;         // threads of a CTA whose only group is beyond 256 lanes
+constexpr int kWide = 512;         // threads of a CTA for the widest segments
 constexpr int kSms = 148;
 constexpr int kDropCtas = 4;       // CTAs per SM of k_drop
 constexpr int kMaxSmem = 231 * 1000;  // dynamic shared memory of a CTA (the rest of 227 KB is static)
@@ -98,13 +98,12 @@ __device__ __forceinline__ float total(const f2 (&v)[P]) {
   return lo(s[0]) + hi(s[0]);
 }
 
-// Sums of K values over W (a power of two) consecutive warps, to all their threads, by
+// Sums of K values, equal in a warp, over W (a power of two) consecutive warps, to all their threads, by
 // way of part[2][warps of the CTA][K] in shared memory: calls alternate between the two halves, and
 // none can be two calls ahead of another warp, so one barrier a call is enough.
 template <int K, class Sync>
 __device__ __forceinline__ void warps_sum(float (&v)[K], float* part, int& flip, int warp, int first, int W,
                                           int warps, Sync sync) {
-  group_sum(v, 32);
   float* half = part + flip * warps * K;
   flip ^= 1;
   if ((threadIdx.x & 31) == 0)
@@ -153,9 +152,8 @@ struct Place {
   }
   template <int K>
   __device__ __forceinline__ void sum(float (&v)[K]) const {
-    if (G <= 32) {
-      group_sum(v, G);
-    } else {
+    group_sum(v, G);
+    if (G > 32) {
       const int warp = (int)threadIdx.x >> 5, W = G >> 5;
       warps_sum(v, part, flip, warp, warp & ~(W - 1), W, TH / 32, [&] { sync(); });
     }
@@ -337,12 +335,27 @@ struct Out {
       if (EDGE ? bits == all : bits != 0) {
         *reinterpret_cast<uint4*>(p + j * pack_step) = make_uint4(w[0], w[1], w[2], w[3]);
       } else if (EDGE && bits) {
+        // a cut pack in the widest pieces that it has (single elements: twice the time, 50000 x 145 f16)
+        char* to = p + j * pack_step;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (bits >> i & 1) {
-            if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(p + j * pack_step)[i] = w[i];
-            else reinterpret_cast<uint16_t*>(p + j * pack_step)[i] = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t half = (1u << (V / 2)) - 1, bh = bits >> (h * (V / 2)) & half;
+          if (bh == half) {
+            *reinterpret_cast<uint2*>(to + 8 * h) = make_uint2(w[2 * h], w[2 * h + 1]);
+            continue;
           }
+#pragma unroll
+          for (int q = 2 * h; q < 2 * h + 2; ++q) {
+            if constexpr (sizeof(T) == 4) {
+              if (bits >> q & 1) reinterpret_cast<uint32_t*>(to)[q] = w[q];
+            } else {
+              const uint32_t bq = bits >> (2 * q) & 3u;
+              if (bq == 3u) reinterpret_cast<uint32_t*>(to)[q] = w[q];
+              else if (bq == 1u) reinterpret_cast<uint16_t*>(to)[2 * q] = (uint16_t)w[q];
+              else if (bq == 2u) reinterpret_cast<uint16_t*>(to)[2 * q + 1] = (uint16_t)(w[q] >> 16);
+            }
+          }
+        }
       }
     }
   }
@@ -365,22 +378,34 @@ __device__ __forceinline__ uint32_t valid_bits(const P& at) {
   return bits;
 }
 
-// A channel vector expanded per element in shared memory, element s at [shift + s] of n (`missing`
-// where there is no vector, zeros outside the segment).
-__device__ __forceinline__ void expand(float* to, int n, const float* vec, const Channels& ch, int S, int shift,
-                                       float missing) {
-  // eight loads on the way at a time: this is a CTA's first wait for memory
-  for (int i0 = threadIdx.x; i0 < n; i0 += 8 * blockDim.x) {
-    float v[8];
+// K channel vectors expanded per element in shared memory, one behind the other, element s at [shift +
+// s] of n (`missing` where there is no vector, zeros outside the segment).  All loads of a batch are on
+// the way together: this is a CTA's first wait for memory.
+template <int K>
+__device__ __forceinline__ void expand(float* to, int n, const float* const (&vec)[K], const float (&missing)[K],
+                                       const Channels& ch, int S, int shift) {
+  constexpr int U = 16 / K;
+  for (int i0 = threadIdx.x; i0 < n; i0 += U * blockDim.x) {
+    float v[U][K];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int s = i0 + k * (int)blockDim.x - shift;
-      v[k] = s < 0 || s >= S ? 0.f : vec ? vec[ch.of(s)] : missing;
+    for (int u = 0; u < U; ++u) {
+      const int s = i0 + u * (int)blockDim.x - shift;
+      const bool in = s >= 0 && s < S;
+      const int c = in ? ch.of(s) : 0;
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[u][k] = !in ? 0.f : vec[k] ? vec[k][c] : missing[k];
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (i0 + k * (int)blockDim.x < n) to[i0 + k * blockDim.x] = v[k];
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (i0 + u * (int)blockDim.x < n) to[k * n + i0 + u * blockDim.x] = v[u][k];
   }
+}
+
+// A parameter vector from a block's first channel on.
+__device__ __forceinline__ const float* from_channel(const float* v, int first) {
+  return v && first >= 0 ? v + first : nullptr;
 }
 
 // Pairs of an expanded vector at a lane's elements.
@@ -397,52 +422,58 @@ __device__ __forceinline__ void lookup(f2 (&w)[V * J / 2], const float* vec, con
     }
 }
 
-// Keep bits of a segment's channel groups (four channels each, one byte per group) in shared
-// memory: each group's counter is drawn once, whatever the layout and the number of components.
+// What is kept of a segment's channels, in shared memory: each group of four channels is drawn once,
+// whatever the layout and the number of components.  Where packs lie inside one component and start
+// on a multiple of four channels, a byte holds a group's four bits; else a byte stands for a channel,
+// and the lanes know the channels of their elements.
 template <int V, int J>
 struct Mask {
   unsigned char* m;   // this group's bytes
-  bool quads;         // packs lie inside one component and start on a multiple of four channels
+  bool quads;
   uint64_t off;
+  uint32_t of[J * V / 2];  // channels of the lane's elements, two per word (quads: of the packs)
   template <class P>
-  __device__ __forceinline__ Mask(unsigned char* all, const P& at, const NodeDesc& D, const Drop& drop) {
-    m = all + at.group * ((at.B.C + 3) / 4);
+  __device__ __forceinline__ Mask(unsigned char* all, const P& at, const NodeDesc& D, const Drop& drop,
+                                  const Channels& ch, uint32_t valid) {
+    m = all + at.group * ((at.B.C + 3) / 4 * 4);
     quads = at.shift == 0 && (at.B.d == 1 || (!D.mul_ir && at.B.C % V == 0));
     off = drop.mode == 1 ? drop_offset(drop) : 0;
+#pragma unroll
+    for (int e = 0; e < J * V; e += 2) {
+      uint32_t c[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        c[i] = valid >> (e + i) & 1 ? ch.of(at.template elem<V>((e + i) / V) + (e + i) % V) : 0;
+      of[e / 2] = c[0] | c[1] << 16;
+    }
   }
   // keep bits of a lane's elements in a row, lowest first
   template <class P>
-  __device__ __forceinline__ uint32_t bits(const Drop& drop, const P& at, const Channels& ch, uint32_t row,
-                                           uint32_t valid) {
+  __device__ __forceinline__ uint32_t bits(const Drop& drop, const P& at, uint32_t row) {
     if (drop.mode != 1) return drop.mode == 0 ? ~0u : 0u;
     at.sync();  // the previous row's readers are done
     const int groups = (at.B.C + 3) / 4;
     for (int g = at.lane; g < groups; g += at.G) {
       const uint4 w = drop_words(drop, off, at.B.grp0 + g, row);
-      m[g] = (w.x >= drop.threshold ? 1 : 0) | (w.y >= drop.threshold ? 2 : 0) | (w.z >= drop.threshold ? 4 : 0) |
-             (w.w >= drop.threshold ? 8 : 0);
+      const uint32_t k0 = w.x >= drop.threshold, k1 = w.y >= drop.threshold, k2 = w.z >= drop.threshold,
+                     k3 = w.w >= drop.threshold;
+      if (quads) m[g] = (unsigned char)(k0 | k1 << 1 | k2 << 2 | k3 << 3);
+      else *reinterpret_cast<uint32_t*>(m + 4 * g) = k0 | k1 << 8 | k2 << 16 | k3 << 24;
     }
     at.sync();
     uint32_t keep = 0;
     if (quads) {
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        const int c = valid >> (j * V) & 1 ? ch.of(at.template elem<V>(j)) >> 2 : 0;
+        const uint32_t g = (of[j * V / 2] & 0xffffu) >> 2;
         // a cut last pack reads bytes of groups that are not there: its bits are not used
 #pragma unroll
-        for (int i = 0; i < V / 4; ++i) keep |= (uint32_t)m[c + i] << (j * V + 4 * i);
+        for (int i = 0; i < V / 4; ++i) keep |= (uint32_t)m[g + i] << (j * V + 4 * i);
       }
     } else {
-#pragma unroll 1
-      for (int j = 0; j < J; ++j) {
-        const int s = at.template elem<V>(j);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (valid >> (j * V + i) & 1) {
-            const int c = ch.of(s + i);
-            keep |= ((uint32_t)m[c >> 2] >> (c & 3) & 1u) << (j * V + i);
-          }
-      }
+      for (int e = 0; e < J * V; ++e)
+        keep |= (uint32_t)m[e % 2 ? of[e / 2] >> 16 : of[e / 2] & 0xffffu] << e;
     }
     return keep;
   }
@@ -486,13 +517,15 @@ __host__ __device__ constexpr int rows_bytes(int elems, int arrays, int packs, b
 // a vector's elements as far as any lane reads them
 __host__ __device__ constexpr int vector_bytes(int elems, int lg) { return (elems << lg) * 4; }
 constexpr int kPartBytes = 2 * (kWide / 32) * 5 * 4;  // up to five sums at a time
-constexpr int mask_bytes(int elems, int threads) { return threads * elems / 4 + threads + 8; }
+constexpr int mask_bytes(int elems, int threads) { return threads * elems + 4 * threads; }
 
 extern __shared__ __align__(16) char g_smem[];
 
 enum Pass { PASS_FWD = NORM_FORWARD, PASS_BWD = NORM_BACKWARD, PASS_DBL = NORM_DOUBLE_BACKWARD };
 
 // CTAs of 256 threads that an SM is to hold (a bound on the registers).
+// (Three in the forward up to 8 elements, two else: more are not faster, the backward's of 8
+// elements are slower by 5 to 15 %.)
 constexpr int min_ctas(Pass pass, int elems) { return pass == PASS_FWD && elems <= 8 ? 3 : 2; }
 
 #define TPC_NODE_KERNEL(TH, PASS, ELEMS) \
@@ -516,12 +549,12 @@ TPC_NODE_KERNEL(TH, PASS_FWD, 16 / sizeof(T) * J)
   if constexpr (DROP) rows.start(g_smem, D, at, N, {A.x, A.residual});
   else rows.start(g_smem, D, at, N, {A.x});
   if constexpr (NORM) {
-    expand(sw, E << at.lg, A.weight ? A.weight + B.chan0 : nullptr, ch, B.S, at.shift, 1.f);
-    expand(sb, E << at.lg, centred && A.bias ? A.bias + B.bias0 : nullptr, ch, B.S, at.shift, 0.f);
+    expand<2>(sw, E << at.lg, {from_channel(A.weight, B.chan0), from_channel(A.bias, B.bias0)}, {1.f, 0.f}, ch, B.S,
+              at.shift);
     __syncthreads();
   }
-  Mask<V, J> mask(reinterpret_cast<unsigned char*>(NORM ? sb + (E << at.lg) : sw), at, D, drop);
   const uint32_t valid = valid_bits<V, J>(at);
+  Mask<V, J> mask(reinterpret_cast<unsigned char*>(NORM ? sb + (E << at.lg) : sw), at, D, drop, ch, valid);
   const Inner<T, J, EDGE> inner(valid);
   Out<T, J, TH, EDGE> y(NORM ? A.y : nullptr, D, at), z(DROP ? A.z : nullptr, D, at);
   f2 w[NORM ? P : 1], b[NORM ? P : 1];
@@ -535,7 +568,7 @@ TPC_NODE_KERNEL(TH, PASS_FWD, 16 / sizeof(T) * J)
     f2 v[P];
     inner.get(rows, 0, v);
     if constexpr (DROP) {
-      apply_mask(v, mask.bits(drop, at, ch, n, valid), drop.scale);
+      apply_mask(v, mask.bits(drop, at, n), drop.scale);
       if (A.residual) {
         f2 r[P];
         inner.get(rows, R - 1, r);
@@ -567,36 +600,36 @@ TPC_NODE_KERNEL(TH, PASS_FWD, 16 / sizeof(T) * J)
   rows.finish();
 }
 
-// Adds the lanes' sums over rows of a CTA and writes them per channel.
+// Adds the lanes' sums over rows of a CTA and writes them per channel.  Short code: it runs once, and
+// is waited for as it is fetched (12,700 cycles with shuffles unrolled over the elements, 4096x0e).
 template <int V, int J, int TH, bool EDGE>
 __device__ __forceinline__ void write_sums(const f2 (&sums)[V * J / 2], float* smem, float* out,
                                            const Place<TH, EDGE>& at, const Channels& ch) {
   constexpr int E = V * J;
-  const int S = at.B.S, G = at.G;
-  float acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = e % 2 ? hi(sums[e / 2]) : lo(sums[e / 2]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    if (G <= o) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], o);
-    }
+  const int lanes_e = E << at.lg, copies = TH >> at.lg;  // a group's elements, groups
   __syncthreads();  // the ring, or earlier sums, have been read
-  // copies of the segment: one per warp, or per group of several warps
-  const int copies = G <= 32 ? TH / 32 : TH / G, copy = G <= 32 ? (int)threadIdx.x >> 5 : at.group;
-  if (G > 32 || ((int)threadIdx.x & 31) < G) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int s = at.template elem<V>(e / V) + e % V;
-      if (s >= 0 && s < S) smem[copy * S + s] = acc[e];
+  for (int j = 0; j < J; ++j)
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const f2 a = sums[(j * V + i) / 2], b = sums[(j * V + i) / 2 + 1];
+      *reinterpret_cast<float4*>(smem + at.group * lanes_e + (j * at.G + at.lane) * V + i) =
+          make_float4(lo(a), hi(a), lo(b), hi(b));
     }
-  }
   __syncthreads();
+  if (copies > 1) {
+    for (int i = threadIdx.x; i < lanes_e; i += TH) {
+      float v = 0.f;
+#pragma unroll 8
+      for (int k = 0; k < copies; ++k) v += smem[k * lanes_e + i];
+      smem[i] = v;  // copy 0: read by this thread alone
+    }
+    __syncthreads();
+  }
+#pragma unroll 1
   for (int c = threadIdx.x; c < at.B.C; c += TH) {
     float v = 0.f;
-    for (int m = 0; m < at.B.d; ++m)
-      for (int k = 0; k < copies; ++k) v += smem[k * S + ch.at(c, m)];
+    for (int m = 0; m < at.B.d; ++m) v += smem[at.shift + ch.at(c, m)];
     out[c] = v;
   }
 }
@@ -624,55 +657,65 @@ TPC_NODE_KERNEL(TH, PASS_BWD, 16 / sizeof(T) * J)
   Ring<T, J, R, TH, EDGE> rows;
   if constexpr (DROP) rows.start(g_smem, D, at, N, {A.x, A.grad_y, A.grad_z});
   else rows.start(g_smem, D, at, N, {A.x, A.grad_y});
-  expand(ws, E << at.lg, A.weight ? A.weight + B.chan0 : nullptr, ch, B.S, at.shift, 1.f);
+  expand<1>(ws, E << at.lg, {from_channel(A.weight, B.chan0)}, {1.f}, ch, B.S, at.shift);
   __syncthreads();
-  Mask<V, J> mask(reinterpret_cast<unsigned char*>(ws + (E << at.lg)), at, D, drop);
   const uint32_t valid = valid_bits<V, J>(at);
+  Mask<V, J> mask(reinterpret_cast<unsigned char*>(ws + (E << at.lg)), at, D, drop, ch, valid);
   const Inner<T, J, EDGE> inner(valid);
-  f2 sw[P], sb[P];
+  constexpr bool HOLD = E <= 8;  // as the registers allow (16 elements spill: 4096x0e bf16 74 us, 69 us without)
+  f2 w[P], sw[P], sb[P];
+  if constexpr (HOLD) lookup<V, J>(w, ws, at);
 #pragma unroll
   for (int p = 0; p < P; ++p) sw[p] = sb[p] = 0;
   Out<T, J, TH, EDGE> gx(A.grad_x, D, at), gr(DROP ? A.grad_residual : nullptr, D, at);
+  float* const sums_w = sums_out(M, B, at.k, A.partial, A.grad_weight, B.chan0, false);
+  float* const sums_b = centred ? sums_out(M, B, at.k, A.partial, A.grad_bias, B.bias0, true) : nullptr;
   for (uint32_t n = at.n; at.more(n, N); n += at.stride) {
     const bool ok = n < N;
     rows.next();
+    // HOLD: grad_y and the weights stay in registers; else their product, and grad_y is read again
     f2 u[P], a[P];
     inner.get(rows, 0, u);
-    {
-      f2 w[P];
-      inner.get(rows, 1, a);
-      lookup<V, J>(w, ws, at);
-      if (centred && ok) {
+    inner.get(rows, 1, a);
+    if (centred && ok) {
 #pragma unroll
-        for (int p = 0; p < P; ++p) sb[p] = add2(sb[p], a[p]);
-      }
-#pragma unroll
-      for (int p = 0; p < P; ++p) a[p] = mul2(a[p], w[p]);
+      for (int p = 0; p < P; ++p) sb[p] = add2(sb[p], a[p]);
     }
+    if constexpr (!HOLD) {
+      lookup<V, J>(w, ws, at);
+#pragma unroll
+      for (int p = 0; p < P; ++p) a[p] = mul2(w[p], a[p]);
+    }
+    const auto product = [&](int p) { return HOLD ? mul2(w[p], a[p]) : a[p]; };  // weight grad_y
+    float ma = 0.f;
     if (centred) {
-      float m[2] = {total(u), total(a)};
+      f2 t[P];
+#pragma unroll
+      for (int p = 0; p < P; ++p) t[p] = product(p);
+      float m[2] = {total(u), total(t)};
       at.sum(m);
       shift_by<V, J, EDGE>(u, -m[0] * inv, valid);
-      shift_by<V, J, EDGE>(a, -m[1] * inv, valid);
+      ma = m[1] * inv;
     }
-    f2 q0 = mul2(u[0], u[0]), q1 = mul2(u[0], a[0]);
+    // mean(a) drops out of mean(a h) in a 0e block: h has no mean
+    f2 q0 = mul2(u[0], u[0]), q1 = mul2(u[0], product(0));
 #pragma unroll
     for (int p = 1; p < P; ++p) {
       q0 = fma2(u[p], u[p], q0);
-      q1 = fma2(u[p], a[p], q1);
+      q1 = fma2(u[p], product(p), q1);
     }
     float q[2] = {lo(q0) + hi(q0), lo(q1) + hi(q1)};
     at.sum(q);
     const float r = rsqrtf(q[0] * inv + D.eps);
     {
       f2 g[P];
-      inner.get(rows, 1, g);   // read again instead of held: the registers carry the sums
-      const f2 r2 = both(r), mh = both(-(r * q[1] * inv));
+      if constexpr (!HOLD) inner.get(rows, 1, g);
+      const f2 r2 = both(r), mh = both(-(r * r * q[1] * inv)), c0 = both(-(r * ma));
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const f2 h = mul2(u[p], r2);
-        if (ok) sw[p] = fma2(g[p], h, sw[p]);
-        u[p] = mul2(r2, fma2(h, mh, a[p]));
+        if (ok) sw[p] = fma2(HOLD ? a[p] : g[p], h, sw[p]);
+        u[p] = fma2(h, mh, fma2(product(p), r2, c0));
       }
     }
     if constexpr (DROP) {
@@ -684,7 +727,7 @@ TPC_NODE_KERNEL(TH, PASS_BWD, 16 / sizeof(T) * J)
       }
       if (gr && ok) gr.put(u, valid);
       gr.next();
-      if (gx) apply_mask(u, mask.bits(drop, at, ch, n, valid), drop.scale);
+      if (gx) apply_mask(u, mask.bits(drop, at, n), drop.scale);
     }
     if (gx && ok) gx.put(u, valid);
     gx.next();
@@ -693,11 +736,8 @@ TPC_NODE_KERNEL(TH, PASS_BWD, 16 / sizeof(T) * J)
   rows.finish();
   cudaTriggerProgrammaticLaunchCompletion();
   float* smem = reinterpret_cast<float*>(g_smem);
-  if (float* out = sums_out(M, B, at.k, A.partial, A.grad_weight, B.chan0, false))
-    write_sums<V, J>(sw, smem, out, at, ch);
-  if (centred)
-    if (float* out = sums_out(M, B, at.k, A.partial, A.grad_bias, B.bias0, true))
-      write_sums<V, J>(sb, smem, out, at, ch);
+  if (sums_w) write_sums<V, J>(sw, smem, sums_w, at, ch);
+  if (sums_b) write_sums<V, J>(sb, smem, sums_b, at, ch);
 }
 
 template <class T, int J, int TH, bool EDGE>
@@ -715,9 +755,9 @@ TPC_NODE_KERNEL(TH, PASS_DBL, 16 / sizeof(T) * J)
   float *ts = ws + (E << at.lg), *bs = ts + (E << at.lg);
   Ring<T, J, 3, TH, EDGE> rows;
   rows.start(g_smem, D, at, N, {A.x, A.grad_y, A.gg_x});
-  expand(ws, E << at.lg, A.weight ? A.weight + B.chan0 : nullptr, ch, B.S, at.shift, 1.f);
-  expand(ts, E << at.lg, A.gg_weight ? A.gg_weight + B.chan0 : nullptr, ch, B.S, at.shift, 0.f);
-  expand(bs, E << at.lg, centred && A.gg_bias ? A.gg_bias + B.bias0 : nullptr, ch, B.S, at.shift, 0.f);
+  expand<3>(ws, E << at.lg,
+            {from_channel(A.weight, B.chan0), from_channel(A.gg_weight, B.chan0), from_channel(A.gg_bias, B.bias0)},
+            {1.f, 0.f, 0.f}, ch, B.S, at.shift);
   __syncthreads();
   const uint32_t valid = valid_bits<V, J>(at);
   const Inner<T, J, EDGE> inner(valid);
@@ -725,6 +765,7 @@ TPC_NODE_KERNEL(TH, PASS_DBL, 16 / sizeof(T) * J)
 #pragma unroll
   for (int p = 0; p < P; ++p) sw[p] = 0;
   Out<T, J, TH, EDGE> gx(A.grad_x, D, at), gg(A.grad_grad_y, D, at);
+  float* const sums_w = sums_out(M, B, at.k, A.partial, A.grad_weight, B.chan0, false);
   for (uint32_t n = at.n; at.more(n, N); n += at.stride) {
     const bool ok = n < N;
     rows.next();
@@ -793,8 +834,7 @@ TPC_NODE_KERNEL(TH, PASS_DBL, 16 / sizeof(T) * J)
   }
   rows.finish();
   cudaTriggerProgrammaticLaunchCompletion();
-  if (float* out = sums_out(M, B, at.k, A.partial, A.grad_weight, B.chan0, false))
-    write_sums<V, J>(sw, reinterpret_cast<float*>(g_smem), out, at, ch);
+  if (sums_w) write_sums<V, J>(sw, reinterpret_cast<float*>(g_smem), sums_w, at, ch);
 }
 
 // ---- dropout alone in 16 bits, blocks whose channels come in whole packs: a thread owns V channels of
@@ -888,6 +928,7 @@ __global__ void __launch_bounds__(kThreads, kDropCtas)
 template <int K>
 __device__ __forceinline__ void cta_sum(float (&v)[K], int& flip) {
   __shared__ float part[2 * (kThreads / 32) * K];
+  group_sum(v, 32);
   warps_sum(v, part, flip, threadIdx.x >> 5, 0, kThreads / 32, kThreads / 32, [] { __syncthreads(); });
 }
 
@@ -1119,7 +1160,7 @@ __global__ void __launch_bounds__(32 * kShares)
 
 // ---- launch plan ----
 
-enum Kind { KIND_GROUP, KIND_WIDE, KIND_ANY };  // 256 threads, one group of 512, any width
+enum Kind { KIND_GROUP, KIND_WIDE, KIND_ANY };  // 256 threads, 512 threads, any width
 
 struct Launch {
   Kind kind;
@@ -1174,12 +1215,15 @@ LaunchPlan plan_launches(const Shape& sh, const NodeDesc& D, long long N) {
   while (P.edge && (long long)R * D.dim % V != 0) R *= 2;
   const int pad = P.edge ? V - 1 : 0;
   const int jmax = most_packs(sh.pass == PASS_DBL, sh.esize);
+  // Most lanes of a segment in CTAs of 256 threads.  Wider ones share CTAs of 512 in the passes with
+  // sums: half the partial sums (backward 8192 x 4096 bf16: 63 us, 65 us).
+  const int narrow = sums ? 128 : kThreads;
   Kind kind[MAX_BLOCKS];
   for (int b = 0; b < D.n_blocks; ++b) {
     const int S = D.b[b].S + pad;
-    kind[b] = S <= kThreads * V * jmax                                                         ? KIND_GROUP
-              : S <= kWide * V * jmax && sh.smem(jmax, kWide, log2_lanes(kWide, 1)) <= kMaxSmem ? KIND_WIDE
-                                                                                               : KIND_ANY;
+    kind[b] = S <= narrow * V * jmax                                                  ? KIND_GROUP
+              : S <= kWide * V * jmax && sh.smem(jmax, kWide, log2_lanes(S, V * jmax)) <= kMaxSmem ? KIND_WIDE
+                                                                                                  : KIND_ANY;
   }
   for (Kind kd : {KIND_GROUP, KIND_WIDE, KIND_ANY}) {
     Launch L{};
@@ -1196,13 +1240,13 @@ LaunchPlan plan_launches(const Shape& sh, const NodeDesc& D, long long N) {
       for (int k = 0; k < M.n; ++k) M.lg[k] = log2_lanes(kThreads, 1);
     } else {
       // Fewest lane-packs per row (a segment's lanes are a power of two); of equal ones the most
-      // packs per lane, but 12 elements in the passes with sums and dropout alone (fused backward 50000 x 592 f32: 104
-      // us, 112 us with 16), and 8 off the boundary, where each element costs more instructions
-      // (backward 50000 x 145 f32: 30 us, 32 us with 12; f16 mul_ir: 35 us, 41 us with 16).
-      const int lg_max = log2_lanes(L.threads, 1), few = P.edge ? 8 : sums || !sh.norm ? 12 : 16;
+      // packs per lane, but 12 elements in the passes with sums and in dropout alone (fused backward
+      // 50000 x 592 f32: 104 us, 112 us with 16), and 8 in the passes with sums off the boundary, whose
+      // masks take registers (backward 50000 x 145 f32: 28 us, 31 us with 12; f16: 26 us, 29 us with 16).
+      const int lg_max = log2_lanes(L.threads, 1), few = P.edge && sums ? 8 : !P.edge && (sums || !sh.norm) ? 12 : 16;
       long long best = -1;
       for (int j = kd == KIND_WIDE ? jmax : 1; j <= jmax; ++j) {
-        if (P.edge && V * j > few && best >= 0) break;
+        if (P.edge && sums && V * j > few && best >= 0) break;
         long long cost = 0;
         bool fits = true;
         for (int k = 0; k < M.n; ++k) {
@@ -1219,7 +1263,7 @@ LaunchPlan plan_launches(const Shape& sh, const NodeDesc& D, long long N) {
       }
       int widest = 0;
       for (int k = 0; k < M.n; ++k) {
-        M.lg[k] = kd == KIND_WIDE ? lg_max : log2_lanes(D.b[M.blk[k]].S + pad, V * L.J);
+        M.lg[k] = log2_lanes(D.b[M.blk[k]].S + pad, V * L.J);
         widest = M.lg[k] > widest ? M.lg[k] : widest;
       }
       L.smem = sh.smem(L.J, L.threads, widest);

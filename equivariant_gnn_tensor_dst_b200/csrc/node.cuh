@@ -94,15 +94,27 @@ struct Channels {
   __device__ __forceinline__ int at(int c, int m) const { return mul_ir ? c * d + m : m * C + c; }
 };
 
-// Sums of K values over groups of G lanes (a power of two, at most 32), to all lanes of a group.
+// Sums of K values over groups of G lanes (a power of two, at most 32), to all lanes of a group.  One
+// branch on G: one a step, and what it takes to bring the lanes together again, cost as much as it
+// saved.
+template <int K>
+__device__ __forceinline__ void group_step(float (&v)[K], int G, int o) {
+  const bool in = G > o;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const float w = __shfl_xor_sync(0xffffffffu, v[k], o);
+    v[k] += in ? w : 0.f;
+  }
+}
 template <int K>
 __device__ __forceinline__ void group_sum(float (&v)[K], int G) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    if (G > o) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-    }
+  if (G > 8) {
+    group_step(v, G, 16);
+    group_step(v, G, 8);
+  }
+  group_step(v, G, 4);
+  group_step(v, G, 2);
+  group_step(v, G, 1);
 }
 
 }  // namespace tpc
