@@ -130,7 +130,7 @@ tpconv_status tpconv_node_plan_create(tpconv_node_plan_t* out, const char* irrep
   if (!out || !irreps) return TPCONV_ERR_INVALID_ARG;
   if (dtype != TPCONV_DTYPE_F32 && dtype != TPCONV_DTYPE_BF16 && dtype != TPCONV_DTYPE_F16)
     return TPCONV_ERR_UNSUPPORTED;
-  if (!(eps > 0.f) || !std::isfinite(eps)) return TPCONV_ERR_INVALID_ARG;
+  if (!(eps > 0.f) || !std::isnormal(eps)) return TPCONV_ERR_INVALID_ARG;
   try {
     std::vector<Block> blocks;
     const tpconv_status st = parse_irreps(irreps, blocks);

@@ -34,7 +34,8 @@
  *    each output is rounded once.  Sums of squares beyond float32's range give r = 0.
  *  - Every compute call is asynchronous on `stream`, allocates nothing, does not synchronise
  *    and may be captured into a CUDA graph.  Results are deterministic (no floating-point
- *    atomics; fixed order), and a row's results do not depend on the other rows.
+ *    atomics; fixed order).  A row's results do not depend on the other rows; where rows do not
+ *    start on 16-byte boundaries, their last bits may depend on the row's number modulo 8.
  *  - Gradient outputs are overwritten, never accumulated; a NULL one is not computed.  With
  *    N = 0 the weight and bias gradients are zeroed.
  *  - Outputs must not overlap inputs or each other (TPCONV_ERR_INVALID_ARG), except that
@@ -76,8 +77,8 @@ typedef struct {
 } tpconv_dropout_spec;
 
 /* Plan of rows given by an irreps string (as tpconv_plan_create: orders l <= 3, at most 16
- * blocks), a storage type and the norm's eps (finite, > 0).  Host memory only; *out is set
- * only on success.  Errors: PARSE, UNSUPPORTED (order, blocks, type), INVALID_ARG.        */
+ * blocks), a storage type and the norm's eps (a normal float32 > 0).  Host memory only; *out is
+ * set only on success.  Errors: PARSE, UNSUPPORTED (order, blocks, type), INVALID_ARG.        */
 tpconv_status tpconv_node_plan_create(tpconv_node_plan_t* out, const char* irreps, int32_t dtype,
                                       float eps);
 

@@ -23,7 +23,8 @@ MIXED, ODD = "128x0e+64x1o+32x2e+16x3o", "37x0e+19x1o+6x2e+3x3o"
 SEED, OFFSET = 0xFEDCBA9876543210, (1 << 40) + 3
 CASES = [("8x0e+8x1o+8x2e", 64, 0.1), (MIXED, 60, 0.5), (ODD, 33, 0.3), ("1x0e", 9, 0.5), ("1x1o", 9, 0.5),
          ("5x0o+2x0e+3x3o", 21, 0.9), ("4096x0e", 3, 0.2), ("12x1o+4x0e", 1, 0.25), ("20001x0e", 1, 0.5),
-         (ODD, 17, 0.0), (ODD, 17, 1.0), ("64x0e", 700, 0.1), ("4100x1o", 2, 0.5)]
+         (ODD, 17, 0.0), (ODD, 17, 1.0), ("64x0e", 700, 0.1), ("4100x1o", 2, 0.5), ("6x0e+10x1o", 300, 0.4),
+         ("1001x0e", 20, 0.2), ("2048x0e+4x1o", 30, 0.6)]
 
 
 def _drop(p, step=None):
@@ -49,7 +50,9 @@ def test_dropout_float32(torch, irreps, n, p, layout):
 
 
 @pytest.mark.parametrize("dtype", TYPES[1:])
-@pytest.mark.parametrize("irreps,n,p", [(MIXED, 40, 0.1), (ODD, 33, 0.5), ("4096x0e", 2, 0.3), ("1x0e", 3, 0.5)])
+@pytest.mark.parametrize("irreps,n,p", [(MIXED, 40, 0.1), (ODD, 33, 0.5), ("4096x0e", 2, 0.3), ("1x0e", 3, 0.5),
+                                        ("8x0e+16x1o+8x2e+24x3o", 500, 0.3), ("3000x0e", 3, 0.5), ("8x3o", 17, 1.0),
+                                        ("40x1o", 19, 0.0), ("12x0e+4x2e", 90, 0.25)])
 @pytest.mark.parametrize("layout", ["ir_mul", "mul_ir"])
 def test_dropout_16_bit(torch, irreps, n, p, dtype, layout):
     from equivariant_gnn_tensor_dst_b200 import binding as B

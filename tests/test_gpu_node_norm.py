@@ -23,7 +23,10 @@ def torch():
 MIXED, ODD = "128x0e+64x1o+32x2e+16x3o", "37x0e+19x1o+6x2e+3x3o"
 SHAPES = [("8x0e+8x1o+8x2e", 64), (MIXED, 300), (ODD, 33), ("1x0e", 5), ("1x1o", 5), ("2x0o+3x0e+1x1e", 7),
           ("4096x0e", 9), ("1023x0e", 3), ("12x0e+12x1o", 1), ("600x1o+5x0e", 6), ("5x3o", 4000), ("64x0e", 3001),
-          ("128x0e+128x1o+128x2e", 700), ("10000x0e+8x1o", 3), ("20001x0e", 2), ("9000x2e", 2)]
+          ("128x0e+128x1o+128x2e", 700), ("10000x0e+8x1o", 3), ("20001x0e", 2), ("9000x2e", 2),
+          # groups of 2, 4, 8 and 16 warps, on the boundary and off it, several rows a CTA and many
+          ("1024x0e", 650), ("1001x0e", 900), ("2048x0e", 400), ("1999x0o", 350), ("4096x0e", 500), ("3999x0e", 310),
+          ("8192x0e", 160), ("8001x0e", 9), ("2700x1o", 5), ("130x2e+65x1o+700x3o", 40), ("16x0e+4096x0e+1x1o", 7)]
 
 
 def _all_passes(p):
@@ -60,7 +63,9 @@ def test_shapes(irreps, n, layout):
 @pytest.mark.parametrize("irreps,n,layout", [(MIXED, 200, "ir_mul"), (ODD, 65, "mul_ir"), (ODD, 64, "ir_mul"),
                                              ("4096x0e", 40, "ir_mul"), ("64x0e+64x1o+64x2e", 333, "mul_ir"),
                                              ("1x0e+1x1o", 1, "ir_mul"), ("20001x0e", 2, "ir_mul"),
-                                             ("8x0e+24x1o", 1000, "ir_mul")])
+                                             ("8x0e+24x1o", 1000, "ir_mul"), ("1024x0e+128x1o", 300, "ir_mul"),
+                                             ("8192x0e", 150, "ir_mul"), ("7001x0e", 20, "ir_mul"),
+                                             ("2049x0e+3x2e", 170, "mul_ir"), ("128x0e+128x1o+128x2e", 900, "mul_ir")])
 def test_16_bit(irreps, n, layout, dtype):
     _all_passes(Problem(irreps, n, dtype, layout))
 
@@ -226,6 +231,120 @@ def test_capture_replay_and_streams(torch):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, outs)) and not torch.equal(got[1], ref[1])
     del graph
+
+
+def test_first_call_captured(torch):
+    """A process whose first calls are made while a graph is captured (kernels not loaded, shared
+    memory not yet allowed), replayed, against the same calls afterwards."""
+    import subprocess
+    import sys
+    code = """
+import torch
+from equivariant_gnn_tensor_dst_b200 import binding as B
+plan = B.NodePlan("128x0e+64x1o+32x2e+16x3o+4096x0e")
+x, gy = (torch.randn(600, plan.dim, device="cuda") for _ in range(2))
+w, b = torch.rand(plan.channels, device="cuda"), torch.rand(plan.biases, device="cuda")
+d, ws = B.Dropout(0.3, 5), B.workspace(plan.workspace_bytes(600), x.device)
+E = torch.empty_like
+o = [E(x), E(x), E(w), E(b), E(x), E(w), E(x), E(x), E(x), E(x), E(x), E(w), E(b)]
+def step():
+    B.tpconv_norm_forward(plan, x, w, b, out=o[0])
+    B.tpconv_norm_backward(plan, x, w, gy, ws=ws, outputs=o[1:4])
+    B.tpconv_norm_double_backward(plan, x, w, gy, gy, w, b, ws=ws, outputs=o[4:7])
+    B.tpconv_dropout_norm_forward(plan, x, d, residual=gy, weight=w, bias=b, outputs=o[7:9])
+    B.tpconv_dropout_norm_backward(plan, x, w, gy, d, grad_z=gy, ws=ws, outputs=o[9:13])
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    step()
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in o]
+step()
+torch.cuda.synchronize()
+assert all(torch.equal(s, t) for s, t in zip(got, o))
+print("captured ok")
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured ok" in r.stdout, r.stdout + r.stderr
+
+
+def test_two_streams_and_threads(torch):
+    """Calls with one plan from two threads on two streams, each with its own workspace, give what
+    they give one after the other."""
+    import threading
+    from equivariant_gnn_tensor_dst_b200 import binding as B
+    p = Problem(MIXED, 3000)
+    grads = [p.rows()[0] for _ in range(2)]
+    ref = [B.tpconv_norm_backward(p.plan, p.x, p.w, g) for g in grads]
+    torch.cuda.synchronize()
+    got, streams = [[], []], [torch.cuda.Stream() for _ in range(2)]
+
+    def work(i):
+        with torch.cuda.stream(streams[i]):
+            ws = B.workspace(p.plan.workspace_bytes(p.n), p.x.device)
+            for _ in range(20):
+                got[i].append(B.tpconv_norm_backward(p.plan, p.x, p.w, grads[i], ws=ws))
+        streams[i].synchronize()
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    for i in range(2):
+        for r in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(r, ref[i]))
+
+
+def test_two_graphs_share_a_workspace(torch):
+    """Graphs captured with the same workspace, replayed one after the other in either order."""
+    from equivariant_gnn_tensor_dst_b200 import binding as B
+    p, q = Problem(MIXED, 2000), Problem(ODD, 900)
+    (gp, _), (gq, _) = p.rows(), q.rows()
+    ws = B.workspace(max(p.plan.workspace_bytes(p.n), q.plan.workspace_bytes(q.n)), p.x.device)
+    calls = [(a, g, tuple(torch.empty_like(t) for t in (a.x, a.w, a.b))) for a, g in ((p, gp), (q, gq))]
+    ref = [[t.clone() for t in B.tpconv_norm_backward(a.plan, a.x, a.w, g)] for a, g, _ in calls]
+    graphs = []
+    for a, g, o in calls:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            B.tpconv_norm_backward(a.plan, a.x, a.w, g, ws=ws, outputs=o)
+        graphs.append(graph)
+    for order in ((0, 1), (1, 0), (0, 0, 1, 1)):
+        for _, _, o in calls:
+            for t in o:
+                t.fill_(float("nan"))
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for (_, _, o), r in zip(calls, ref):
+            assert all(torch.equal(s, t) for s, t in zip(o, r))
+    del graphs
+
+
+def test_guard_bands(torch):
+    """Nothing outside the outputs is written, whatever the alignment of rows and blocks."""
+    from equivariant_gnn_tensor_dst_b200 import binding as B
+    for irreps in (MIXED, ODD, "1x0e", "3x0e+1x1o", "1001x0e", "8001x0e"):
+        for dtype in TYPES:
+            for n in (1, 2, 7, 33):
+                p = Problem(irreps, n, dtype)
+                gy, _ = p.rows()
+                size, pad = n * p.plan.dim, 64
+                whole = [torch.full((size + 2 * pad,), 9.0, dtype=p.x.dtype, device="cuda") for _ in range(3)]
+                outs = [t[pad:pad + size].view(n, p.plan.dim) for t in whole]
+                B.tpconv_norm_forward(p.plan, p.x, p.w, p.b, out=outs[0])
+                B.tpconv_norm_double_backward(p.plan, p.x, p.w, gy, gy, need_weight=False,
+                                              outputs=(outs[1], None, outs[2]))
+                B.tpconv_dropout_norm_forward(p.plan, p.x, B.Dropout(0.5, 1), residual=gy, outputs=(outs[1], outs[2]))
+                B.tpconv_dropout_norm_backward(p.plan, p.x, p.w, gy, B.Dropout(0.5, 1),
+                                               outputs=(outs[1], outs[2], None, None))
+                B.tpconv_dropout_forward(p.plan, p.x, B.Dropout(0.5, 1), out=outs[0])
+                for t in whole:
+                    assert bool((t[:pad] == 9.0).all()) and bool((t[pad + size:] == 9.0).all())
 
 
 def test_64_bit_offsets(torch):

@@ -39,7 +39,7 @@ def test_plan_numbering():
     ("4x0q", 0, 1e-5, PARSE), ("", 0, 1e-5, PARSE), ("0x0e", 0, 1e-5, PARSE), ("4x4e", 0, 1e-5, UNSUPPORTED),
     ("+".join(["1x0e"] * 17), 0, 1e-5, UNSUPPORTED), ("4x0e", 3, 1e-5, UNSUPPORTED), ("4x0e", -1, 1e-5, UNSUPPORTED),
     ("4x0e", 0, 0.0, INVALID), ("4x0e", 0, -1.0, INVALID), ("4x0e", 0, float("nan"), INVALID),
-    ("4x0e", 0, float("inf"), INVALID),
+    ("4x0e", 0, float("inf"), INVALID), ("4x0e", 0, 1e-40, INVALID),
 ])
 def test_plan_errors(irreps, dtype, eps, code):
     h = ctypes.c_void_p()
@@ -165,6 +165,42 @@ def test_nothing_requested_is_a_no_op(plan):
     a = [ptr(0), None, ptr(2)] + [None] * 7
     for name in ("norm_backward", "norm_double_backward", "dropout_norm_backward"):
         assert _calls(plan, N, a, drop, 0)[name]() == OK
+
+
+def test_closed_plan_is_refused():
+    p = binding.NodePlan("8x0e")
+    p.close()
+    assert binding.lib().tpconv_norm_forward(p.handle, 1, ptr(0), None, None, ptr(1), None) == INVALID
+
+
+def test_workspace_of_every_shape_is_bounded():
+    """Widths from one element to a million channels, and both 16-bit and 32-bit rows: no more than
+    the sums of one wave of CTAs."""
+    import torch
+    for irreps in ("1x0e", "4096x0e", "8192x0e", "8191x0e", "20000x0e", "999999x0e", "100x0e+5001x1o+7x3o"):
+        for dtype in (torch.float32, torch.bfloat16):
+            p = binding.NodePlan(irreps, dtype)
+            for n in (1, 7, 1000, 1 << 20, (1 << 31) - 1):
+                assert p.workspace_bytes(n) <= 48 * MIB, (irreps, dtype, n)
+
+
+def test_threads_share_a_plan(plan):
+    """Plans are read only at enqueue time; the workspace query keeps its cache consistent."""
+    import threading
+    want = {n: binding.NodePlan("8x0e+8x1o").workspace_bytes(n) for n in (10, 5000, 70000)}
+    bad = []
+
+    def work(n):
+        for _ in range(300):
+            if plan.workspace_bytes(n) != want[n]:
+                bad.append(n)
+
+    ts = [threading.Thread(target=work, args=(n,)) for n in want for _ in range(2)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not bad
 
 
 def test_binding_refuses_bad_tensors(plan):
