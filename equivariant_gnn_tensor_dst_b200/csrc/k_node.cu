@@ -98,17 +98,19 @@ __device__ __forceinline__ float total(const f2 (&v)[P]) {
   return lo(s[0]) + hi(s[0]);
 }
 
-// Sums of K values, equal in a warp, over W (a power of two) consecutive warps, to all their threads, by
-// way of part[2][warps of the CTA][K] in shared memory: calls alternate between the two halves, and
-// none can be two calls ahead of another warp, so one barrier a call is enough.
+// Sums of K values over W (a power of two) consecutive warps, to all their threads, by way of
+// part[2][warps of the CTA][K] in shared memory: calls alternate between the two halves, and none can
+// be two calls ahead of another warp, so one barrier a call is enough.  (Values folded over the lanes
+// for half the shuffles, and the warps' sums read as vectors, took longer: 4096x0e bf16 68 us, 60 us.)
 template <int K, class Sync>
-__device__ __forceinline__ void warps_sum(float (&v)[K], float* part, int& flip, int warp, int first, int W,
-                                          int warps, Sync sync) {
+__device__ __forceinline__ void warps_sum(float (&v)[K], float* part, int& flip, int first, int W, int warps,
+                                          Sync sync) {
+  group_sum(v, 32);
   float* half = part + flip * warps * K;
   flip ^= 1;
   if ((threadIdx.x & 31) == 0)
 #pragma unroll
-    for (int k = 0; k < K; ++k) half[warp * K + k] = v[k];
+    for (int k = 0; k < K; ++k) half[(threadIdx.x >> 5) * K + k] = v[k];
   sync();
   const int w = first + ((int)threadIdx.x & (W - 1));
 #pragma unroll
@@ -152,10 +154,11 @@ struct Place {
   }
   template <int K>
   __device__ __forceinline__ void sum(float (&v)[K]) const {
-    group_sum(v, G);
-    if (G > 32) {
-      const int warp = (int)threadIdx.x >> 5, W = G >> 5;
-      warps_sum(v, part, flip, warp, warp & ~(W - 1), W, TH / 32, [&] { sync(); });
+    if (G <= 32) {
+      group_sum(v, G);
+    } else {
+      const int W = G >> 5;
+      warps_sum(v, part, flip, ((int)threadIdx.x >> 5) & ~(W - 1), W, TH / 32, [&] { sync(); });
     }
   }
   // element of a lane's pack j (negative or >= S: not in the segment)
@@ -546,6 +549,7 @@ TPC_NODE_KERNEL(TH, PASS_FWD, 16 / sizeof(T) * J)
   float* sw = reinterpret_cast<float*>(reinterpret_cast<char*>(part) + kPartBytes);
   float* sb = sw + (E << at.lg);
   Ring<T, J, R, TH, EDGE> rows;
+  cudaGridDependencySynchronize();  // nothing before this reads what an earlier kernel may write
   if constexpr (DROP) rows.start(g_smem, D, at, N, {A.x, A.residual});
   else rows.start(g_smem, D, at, N, {A.x});
   if constexpr (NORM) {
@@ -598,6 +602,7 @@ TPC_NODE_KERNEL(TH, PASS_FWD, 16 / sizeof(T) * J)
     rows.done();
   }
   rows.finish();
+  cudaTriggerProgrammaticLaunchCompletion();
 }
 
 // Adds the lanes' sums over rows of a CTA and writes them per channel.  Short code: it runs once, and
@@ -655,6 +660,7 @@ TPC_NODE_KERNEL(TH, PASS_BWD, 16 / sizeof(T) * J)
   const float inv = 1.f / (float)B.S;
   float* ws = reinterpret_cast<float*>(reinterpret_cast<char*>(part) + kPartBytes);
   Ring<T, J, R, TH, EDGE> rows;
+  cudaGridDependencySynchronize();
   if constexpr (DROP) rows.start(g_smem, D, at, N, {A.x, A.grad_y, A.grad_z});
   else rows.start(g_smem, D, at, N, {A.x, A.grad_y});
   expand<1>(ws, E << at.lg, {from_channel(A.weight, B.chan0)}, {1.f}, ch, B.S, at.shift);
@@ -754,6 +760,7 @@ TPC_NODE_KERNEL(TH, PASS_DBL, 16 / sizeof(T) * J)
   float* ws = reinterpret_cast<float*>(reinterpret_cast<char*>(part) + kPartBytes);
   float *ts = ws + (E << at.lg), *bs = ts + (E << at.lg);
   Ring<T, J, 3, TH, EDGE> rows;
+  cudaGridDependencySynchronize();
   rows.start(g_smem, D, at, N, {A.x, A.grad_y, A.gg_x});
   expand<3>(ws, E << at.lg,
             {from_channel(A.weight, B.chan0), from_channel(A.gg_weight, B.chan0), from_channel(A.gg_bias, B.bias0)},
@@ -927,9 +934,8 @@ __global__ void __launch_bounds__(kThreads, kDropCtas)
 
 template <int K>
 __device__ __forceinline__ void cta_sum(float (&v)[K], int& flip) {
-  __shared__ float part[2 * (kThreads / 32) * K];
-  group_sum(v, 32);
-  warps_sum(v, part, flip, threadIdx.x >> 5, 0, kThreads / 32, kThreads / 32, [] { __syncthreads(); });
+  __shared__ __align__(16) float part[2 * (kThreads / 32) * K];
+  warps_sum(v, part, flip, 0, kThreads / 32, kThreads / 32, [] { __syncthreads(); });
 }
 
 // The CTA's block and rows, as Place.
@@ -1269,8 +1275,8 @@ LaunchPlan plan_launches(const Shape& sh, const NodeDesc& D, long long N) {
       L.smem = sh.smem(L.J, L.threads, widest);
       resident = kSms * ctas_per_sm(kd == KIND_WIDE ? 1 : min_ctas(sh.pass, V * L.J), L.smem);
     }
-    // Steps of a CTA: as few as let all CTAs run at a time.  Few rows: one CTA per block, whose sums
-    // need no second launch.
+    // CTAs that run at a time, shared out in proportion to the blocks' steps.  Few rows: one CTA per
+    // block, whose sums need no second launch.
     long long rows[MAX_BLOCKS], total = 0, most = 0;   // rows[k]: CTA steps of block k in a residue class
     for (int k = 0; k < M.n; ++k) {
       const int per_step = kd == KIND_ANY ? 1 : L.threads >> M.lg[k];
@@ -1278,18 +1284,12 @@ LaunchPlan plan_launches(const Shape& sh, const NodeDesc& D, long long N) {
       total += rows[k] * M.classes;
       most = rows[k] > most ? rows[k] : most;
     }
-    long long steps = (total + resident - 1) / resident;
-    if (steps < 1) steps = 1;
-    const auto ctas = [&](int k) { return (rows[k] + steps - 1) / steps * M.classes; };
-    if (sums && M.classes == 1 && most <= 8) {
-      steps = most;
-    } else {
-      for (;; steps += steps / 32 + 1) {
-        long long c = 0;
-        for (int k = 0; k < M.n; ++k) c += ctas(k);
-        if (c <= resident || steps >= most) break;
-      }
-    }
+    const bool few_rows = sums && M.classes == 1 && most <= 4;
+    const auto ctas = [&](int k) -> long long {
+      if (few_rows) return 1;
+      const long long share = total <= resident ? rows[k] : rows[k] * resident / total;
+      return (share < 1 ? 1 : share) * M.classes;
+    };
     M.direct = sums;
     for (int k = 0; k < M.n; ++k) {
       long long c = ctas(k);
@@ -1323,7 +1323,8 @@ struct Call {
   cudaStream_t s;
 };
 
-// Launches one kernel.  Dynamic shared memory beyond 48 KB has to be allowed once per kernel and
+// Launches one kernel, to be set up while the one before it in the stream drains (it waits for that
+// one's end before it touches memory).  Dynamic shared memory beyond 48 KB has to be allowed once per kernel and
 // device (not a stream operation, so a capture may do it).
 template <class... Ps, class... As>
 void launch(void (*kernel)(Ps...), std::atomic<uint64_t>& allowed, const Call& c, const Launch& L, const As&... args) {
@@ -1336,7 +1337,17 @@ void launch(void (*kernel)(Ps...), std::atomic<uint64_t>& allowed, const Call& c
       allowed.fetch_or(bit, std::memory_order_release);
     }
   }
-  kernel<<<L.ctas, L.threads, L.smem, c.s>>>(args...);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(L.ctas);
+  cfg.blockDim = dim3(L.threads);
+  cfg.dynamicSmemBytes = L.smem;
+  cfg.stream = c.s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <class T, int J, int TH, bool EDGE>
