@@ -33,6 +33,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWide = 512;         // threads of a CTA for the widest segments
 constexpr int kSms = 148;
+constexpr int kMostSums = 5;       // sums over a segment taken together
 constexpr int kDropCtas = 4;       // CTAs per SM of k_drop
 constexpr int kMaxSmem = 231 * 1000;  // dynamic shared memory of a CTA (the rest of 227 KB is static)
 constexpr int kAnyParts = 296;     // row ranges of the any-width kernels
@@ -99,22 +100,23 @@ __device__ __forceinline__ float total(const f2 (&v)[P]) {
 }
 
 // Sums of K values over W (a power of two) consecutive warps, to all their threads, by way of
-// part[2][warps of the CTA][K] in shared memory: calls alternate between the two halves, and none can
-// be two calls ahead of another warp, so one barrier a call is enough.  (Values folded over the lanes
+// part[2][half] in shared memory (half: the most floats that a call has, for the CTA's warps): calls
+// alternate between the two halves, and none can be two calls ahead of another warp, so one barrier a
+// call is enough.  (Values folded over the lanes
 // for half the shuffles, and the warps' sums read as vectors, took longer: 4096x0e bf16 68 us, 60 us.)
 template <int K, class Sync>
-__device__ __forceinline__ void warps_sum(float (&v)[K], float* part, int& flip, int first, int W, int warps,
+__device__ __forceinline__ void warps_sum(float (&v)[K], float* part, int half, int& flip, int first, int W,
                                           Sync sync) {
   group_sum(v, 32);
-  float* half = part + flip * warps * K;
+  float* to = part + flip * half;
   flip ^= 1;
   if ((threadIdx.x & 31) == 0)
 #pragma unroll
-    for (int k = 0; k < K; ++k) half[(threadIdx.x >> 5) * K + k] = v[k];
+    for (int k = 0; k < K; ++k) to[(threadIdx.x >> 5) * K + k] = v[k];
   sync();
   const int w = first + ((int)threadIdx.x & (W - 1));
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = half[w * K + k];
+  for (int k = 0; k < K; ++k) v[k] = to[w * K + k];
   group_sum(v, W);
 }
 
@@ -158,7 +160,7 @@ struct Place {
       group_sum(v, G);
     } else {
       const int W = G >> 5;
-      warps_sum(v, part, flip, ((int)threadIdx.x >> 5) & ~(W - 1), W, TH / 32, [&] { sync(); });
+      warps_sum(v, part, kMostSums * (TH / 32), flip, ((int)threadIdx.x >> 5) & ~(W - 1), W, [&] { sync(); });
     }
   }
   // element of a lane's pack j (negative or >= S: not in the segment)
@@ -519,7 +521,7 @@ __host__ __device__ constexpr int rows_bytes(int elems, int arrays, int packs, b
 }
 // a vector's elements as far as any lane reads them
 __host__ __device__ constexpr int vector_bytes(int elems, int lg) { return (elems << lg) * 4; }
-constexpr int kPartBytes = 2 * (kWide / 32) * 5 * 4;  // up to five sums at a time
+constexpr int kPartBytes = 2 * (kWide / 32) * kMostSums * 4;
 constexpr int mask_bytes(int elems, int threads) { return threads * elems + 4 * threads; }
 
 extern __shared__ __align__(16) char g_smem[];
@@ -693,25 +695,49 @@ TPC_NODE_KERNEL(TH, PASS_BWD, 16 / sizeof(T) * J)
       for (int p = 0; p < P; ++p) a[p] = mul2(w[p], a[p]);
     }
     const auto product = [&](int p) { return HOLD ? mul2(w[p], a[p]) : a[p]; };  // weight grad_y
-    float ma = 0.f;
+    float ma = 0.f, q[2];
+    bool second = true;
     if (centred) {
-      f2 t[P];
+      // Groups of several warps wait for one another in a sum: theirs has the second moments as well,
+      // which are exact enough (a few 2^-24 of the mean square) unless the mean is large.
+      const bool once = at.G > 32;
+      f2 t[P], uu = mul2(u[0], u[0]), ut = mul2(u[0], product(0));
 #pragma unroll
       for (int p = 0; p < P; ++p) t[p] = product(p);
-      float m[2] = {total(u), total(t)};
-      at.sum(m);
-      shift_by<V, J, EDGE>(u, -m[0] * inv, valid);
-      ma = m[1] * inv;
-    }
-    // mean(a) drops out of mean(a h) in a 0e block: h has no mean
-    f2 q0 = mul2(u[0], u[0]), q1 = mul2(u[0], product(0));
+      float mu;
+      if (once) {
 #pragma unroll
-    for (int p = 1; p < P; ++p) {
-      q0 = fma2(u[p], u[p], q0);
-      q1 = fma2(u[p], product(p), q1);
+        for (int p = 1; p < P; ++p) {
+          uu = fma2(u[p], u[p], uu);
+          ut = fma2(u[p], t[p], ut);
+        }
+        float m[4] = {total(u), total(t), lo(uu) + hi(uu), lo(ut) + hi(ut)};
+        at.sum(m);
+        mu = m[0] * inv;
+        ma = m[1] * inv;
+        q[0] = m[2] - m[0] * mu;
+        q[1] = m[3] - m[1] * mu;
+        second = !(mu * mu * (float)B.S <= 4.f * q[0]);  // the same in all the group's warps
+      } else {
+        float m[2] = {total(u), total(t)};
+        at.sum(m);
+        mu = m[0] * inv;
+        ma = m[1] * inv;
+      }
+      shift_by<V, J, EDGE>(u, -mu, valid);
     }
-    float q[2] = {lo(q0) + hi(q0), lo(q1) + hi(q1)};
-    at.sum(q);
+    if (second) {
+      // mean(a) drops out of mean(a h) in a 0e block: h has no mean
+      f2 q0 = mul2(u[0], u[0]), q1 = mul2(u[0], product(0));
+#pragma unroll
+      for (int p = 1; p < P; ++p) {
+        q0 = fma2(u[p], u[p], q0);
+        q1 = fma2(u[p], product(p), q1);
+      }
+      q[0] = lo(q0) + hi(q0);
+      q[1] = lo(q1) + hi(q1);
+      at.sum(q);
+    }
     const float r = rsqrtf(q[0] * inv + D.eps);
     {
       f2 g[P];
@@ -935,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, kDropCtas)
 template <int K>
 __device__ __forceinline__ void cta_sum(float (&v)[K], int& flip) {
   __shared__ __align__(16) float part[2 * (kThreads / 32) * K];
-  warps_sum(v, part, flip, 0, kThreads / 32, kThreads / 32, [] { __syncthreads(); });
+  warps_sum(v, part, K * (kThreads / 32), flip, 0, kThreads / 32, [] { __syncthreads(); });
 }
 
 // The CTA's block and rows, as Place.
