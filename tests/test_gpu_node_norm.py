@@ -87,6 +87,25 @@ def test_large_offset():
     assert np.abs(y - ref).max() <= 40 * 2.0 ** -24 * 1000 / np.exp(-1.5) * 2
 
 
+@pytest.mark.parametrize("irreps", ["96x0e", "2048x0e", "4096x0e", "3999x0e"])
+def test_large_offset_backward(irreps):
+    """The same for the backward, in groups of lanes and of several warps, rows of either kind (mean
+    large and not) side by side.  The gradients' scale takes the mean in: tolerance as everywhere."""
+    from equivariant_gnn_tensor_dst_b200 import binding as B
+    p = Problem(irreps, 40)
+    p.x[::3] += 1000.0
+    x64 = p.x.double().cpu().numpy()
+    gy, gy64 = p.rows()
+    gx, gw, gb = B.tpconv_norm_backward(p.plan, p.x, p.w, gy)
+    ex, ew, _ = node.norm_backward(p.R, x64, p.w64, gy64)
+    # an error of the mean, 2^-24 (S / 32 + 16) of |x|, moves every u by as much: relative to the
+    # spread (e^-1.5 at least, r <= e^1.5) that is the error of h, of r and of the mean of a h
+    S = p.R.dim
+    err = 2.0 ** -24 * (S / 32 + 24) * np.abs(x64).mean(axis=1, keepdims=True) * np.exp(1.5)
+    scale = np.exp(1.5) * (np.abs(gy64) + 1) * 2.0 * (1 + np.abs(x64 - x64.mean(axis=1, keepdims=True)) * np.exp(1.5))
+    assert np.all(np.abs(gx.double().cpu().numpy() - ex) <= 6 * (err + tol32(p.R)) * scale)
+
+
 def test_degenerate_rows(torch):
     """Constant, zero, huge, infinite and NaN rows; each touches its own block of its own row."""
     from equivariant_gnn_tensor_dst_b200 import binding
