@@ -100,23 +100,23 @@ __device__ __forceinline__ float total(const f2 (&v)[P]) {
 }
 
 // Sums of K values over W (a power of two) consecutive warps, to all their threads, by way of
-// part[2][half] in shared memory (half: the most floats that a call has, for the CTA's warps): calls
-// alternate between the two halves, and none can be two calls ahead of another warp, so one barrier a
-// call is enough.  (Values folded over the lanes
+// part[2][warps of the CTA][each] in shared memory: calls alternate between the two halves, and none
+// can be two calls ahead of another warp, so one barrier a call is enough.  A warp's place does not
+// depend on K: other groups of the CTA may be at a call with another K.  (Values folded over the lanes
 // for half the shuffles, and the warps' sums read as vectors, took longer: 4096x0e bf16 68 us, 60 us.)
 template <int K, class Sync>
-__device__ __forceinline__ void warps_sum(float (&v)[K], float* part, int half, int& flip, int first, int W,
+__device__ __forceinline__ void warps_sum(float (&v)[K], float* part, int each, int warps, int& flip, int first, int W,
                                           Sync sync) {
   group_sum(v, 32);
-  float* to = part + flip * half;
+  float* to = part + flip * warps * each;
   flip ^= 1;
   if ((threadIdx.x & 31) == 0)
 #pragma unroll
-    for (int k = 0; k < K; ++k) to[(threadIdx.x >> 5) * K + k] = v[k];
+    for (int k = 0; k < K; ++k) to[(threadIdx.x >> 5) * each + k] = v[k];
   sync();
   const int w = first + ((int)threadIdx.x & (W - 1));
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = to[w * K + k];
+  for (int k = 0; k < K; ++k) v[k] = to[w * each + k];
   group_sum(v, W);
 }
 
@@ -160,7 +160,7 @@ struct Place {
       group_sum(v, G);
     } else {
       const int W = G >> 5;
-      warps_sum(v, part, kMostSums * (TH / 32), flip, ((int)threadIdx.x >> 5) & ~(W - 1), W, [&] { sync(); });
+      warps_sum(v, part, kMostSums, TH / 32, flip, ((int)threadIdx.x >> 5) & ~(W - 1), W, [&] { sync(); });
     }
   }
   // element of a lane's pack j (negative or >= S: not in the segment)
@@ -389,6 +389,23 @@ __device__ __forceinline__ uint32_t valid_bits(const P& at) {
 template <int K>
 __device__ __forceinline__ void expand(float* to, int n, const float* const (&vec)[K], const float (&missing)[K],
                                        const Channels& ch, int S, int shift) {
+  if (ch.d == 1 && shift == 0 && S % 4 == 0) {  // channels are elements: four at a time
+    bool aligned = true;
+#pragma unroll
+    for (int k = 0; k < K; ++k) aligned = aligned && (reinterpret_cast<uintptr_t>(vec[k]) & 15u) == 0;
+    if (aligned) {
+      for (int i = 4 * threadIdx.x; i < n; i += 4 * blockDim.x)
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i < S)
+            v = vec[k] ? *reinterpret_cast<const float4*>(vec[k] + i)
+                       : make_float4(missing[k], missing[k], missing[k], missing[k]);
+          *reinterpret_cast<float4*>(to + k * n + i) = v;
+        }
+      return;
+    }
+  }
   constexpr int U = 16 / K;
   for (int i0 = threadIdx.x; i0 < n; i0 += U * blockDim.x) {
     float v[U][K];
@@ -624,6 +641,18 @@ __device__ __forceinline__ void write_sums(const f2 (&sums)[V * J / 2], float* s
           make_float4(lo(a), hi(a), lo(b), hi(b));
     }
   __syncthreads();
+  if (at.B.d == 1 && at.shift == 0 && at.B.C % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & 15u) == 0) {
+    for (int c = 4 * threadIdx.x; c < at.B.C; c += 4 * TH) {  // channels are elements: four at a time
+      float4 v = *reinterpret_cast<const float4*>(smem + c);
+#pragma unroll 4
+      for (int k = 1; k < copies; ++k) {
+        const float4 q = *reinterpret_cast<const float4*>(smem + k * lanes_e + c);
+        v = make_float4(v.x + q.x, v.y + q.y, v.z + q.z, v.w + q.w);
+      }
+      *reinterpret_cast<float4*>(out + c) = v;
+    }
+    return;
+  }
   if (copies > 1) {
     for (int i = threadIdx.x; i < lanes_e; i += TH) {
       float v = 0.f;
@@ -961,7 +990,7 @@ __global__ void __launch_bounds__(kThreads, kDropCtas)
 template <int K>
 __device__ __forceinline__ void cta_sum(float (&v)[K], int& flip) {
   __shared__ __align__(16) float part[2 * (kThreads / 32) * K];
-  warps_sum(v, part, K * (kThreads / 32), flip, 0, kThreads / 32, [] { __syncthreads(); });
+  warps_sum(v, part, K, kThreads / 32, flip, 0, kThreads / 32, [] { __syncthreads(); });
 }
 
 // The CTA's block and rows, as Place.
@@ -1331,7 +1360,7 @@ LaunchPlan plan_launches(const Shape& sh, const NodeDesc& D, long long N) {
         P.parts.blk[i] = M.blk[k];
         P.parts.parts[i] = M.cta0[k + 1] - M.cta0[k];
         P.parts.part0[i] = M.part0[k] = (long long)P.floats;
-        P.floats += (size_t)(P.parts.parts[i] * part_stride(D.b[M.blk[k]]));
+        P.floats += ((size_t)(P.parts.parts[i] * part_stride(D.b[M.blk[k]])) + 3) / 4 * 4;
       }
     P.l[P.n++] = L;
   }

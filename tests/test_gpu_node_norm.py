@@ -87,13 +87,19 @@ def test_large_offset():
     assert np.abs(y - ref).max() <= 40 * 2.0 ** -24 * 1000 / np.exp(-1.5) * 2
 
 
-@pytest.mark.parametrize("irreps", ["96x0e", "2048x0e", "4096x0e", "3999x0e"])
-def test_large_offset_backward(irreps):
+def some_rows(n):
+    """About a third of the rows, in no regular order."""
+    return np.flatnonzero(np.random.default_rng(1).random(n) < 0.33)
+
+
+@pytest.mark.parametrize("irreps,n", [("96x0e", 40), ("1024x0e", 3000), ("2048x0e", 2000), ("4096x0e", 400),
+                                      ("3999x0e", 400)])
+def test_large_offset_backward(irreps, n):
     """The same for the backward, in groups of lanes and of several warps, rows of either kind (mean
-    large and not) side by side.  The gradients' scale takes the mean in: tolerance as everywhere."""
+    large and not) side by side, so that the groups of a CTA are at different sums."""
     from equivariant_gnn_tensor_dst_b200 import binding as B
-    p = Problem(irreps, 40)
-    p.x[::3] += 1000.0
+    p = Problem(irreps, n)
+    p.x[some_rows(n)] += 1000.0
     x64 = p.x.double().cpu().numpy()
     gy, gy64 = p.rows()
     gx, gw, gb = B.tpconv_norm_backward(p.plan, p.x, p.w, gy)
