@@ -1189,8 +1189,9 @@ __global__ void __launch_bounds__(32 * kShares)
   const int c = bias ? i - D.channels : i;
   float* out = bias ? grad_bias : grad_weight;
   bool wanted = out && i < D.channels + D.biases;
-  float v = 0.f;
-  cudaGridDependencySynchronize();  // the partial sums are complete
+  const float* q = nullptr;
+  int parts = 0;
+  long long stride = 0;
   if (wanted) {
     int k = 0;
     for (; k < M.n; ++k) {
@@ -1201,12 +1202,20 @@ __global__ void __launch_bounds__(32 * kShares)
     wanted = k < M.n;  // else the block's only CTA has written the gradient
     if (wanted) {
       const NodeBlock& B = D.b[M.blk[k]];
-      const int parts = M.parts[k];
-      const long long stride = part_stride(B);
-      const float* q = partial + M.part0[k] + (bias ? B.C + c - B.bias0 : c - B.chan0);
-#pragma unroll 8
-      for (int t = ty; t < parts; t += kShares) v += q[t * stride];
+      parts = M.parts[k];
+      stride = part_stride(B);
+      q = partial + M.part0[k] + (bias ? B.C + c - B.bias0 : c - B.chan0);
     }
+  }
+  cudaGridDependencySynchronize();  // the partial sums are complete
+  float v = 0.f;
+  constexpr int kBatch = 10;  // loads on the way at a time: one wait for the CTAs of one wave
+  for (int t = ty; t < parts; t += kBatch * kShares) {
+    float w[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) w[i] = t + i * kShares < parts ? q[(t + i * kShares) * stride] : 0.f;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) v += w[i];
   }
   share[ty][tx] = v;
   __syncthreads();
