@@ -208,13 +208,6 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _raw_stream(stream, device):
-    """The stream handle as an integer (building a torch Stream object costs several microseconds)."""
-    if stream is not None:
-        return stream.cuda_stream
-    return _torch._C._cuda_getCurrentRawStream(device.index)
-
-
 def _need(t, dtype, name):
     import torch
     if t is None:
@@ -561,7 +554,9 @@ def _node_call(device, name, stream, *args):
     if device.index != _torch.cuda.current_device():
         with _torch.cuda.device(device):
             return _node_call(device, name, stream, *args)
-    status = getattr(_lib, name)(*args, _raw_stream(stream, device))
+    # the handle itself: building a torch Stream object costs several microseconds
+    raw = _torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    status = getattr(_lib, name)(*args, raw)
     if status:
         raise TPConvError(status, name)
 

@@ -105,13 +105,6 @@ Prof& prof() {
   return p;
 }
 
-// Kernel launches counted where their number is known only at launch time.
-void prof_add_launches(int c, int n) {
-  Prof& P = prof();
-  std::lock_guard<std::mutex> g(P.mu);
-  if (P.on) P.launches[c] += n;
-}
-
 }  // namespace
 
 int tpc::prof_open(int c, int nk, cudaStream_t s) {
@@ -124,6 +117,12 @@ int tpc::prof_open(int c, int nk, cudaStream_t s) {
   P.cat[slot] = c;
   cudaEventRecord(P.pool[2 * slot], s);
   return slot;
+}
+
+void tpc::prof_count(int c, int n) {
+  Prof& P = prof();
+  std::lock_guard<std::mutex> g(P.mu);
+  if (P.on) P.launches[c] += n;
 }
 
 void tpc::prof_close(int slot, cudaStream_t s) {
@@ -598,7 +597,7 @@ struct Batch {
         }
       }
       err = launch_gemm(h, st);
-      if (h.total_tiles > 0) prof_add_launches(PC_GEMM, h.splits > 1 ? 2 : 1);
+      if (h.total_tiles > 0) prof_count(PC_GEMM, h.splits > 1 ? 2 : 1);
     }
     g.n_problems = 0;
     g.n_segs = 0;

@@ -118,7 +118,7 @@ tpconv_status zero_sums(const tpconv_node_plan* P, float* grad_weight, float* gr
 
 tpconv_status run(const tpconv_node_plan* P, NormPass pass, int64_t N, const NormArgs& A, const Drop* drop,
                   cudaStream_t s) {
-  ProfScope scope(PC_NODE, A.partial ? 2 : 1, s);
+  ProfScope scope(PC_NODE, 0, s);
   return launch_norm(pass, P->dtype, P->desc, N, A, drop, s) == cudaSuccess ? TPCONV_OK : TPCONV_ERR_CUDA;
 }
 
@@ -291,7 +291,7 @@ tpconv_status tpconv_dropout_forward(tpconv_node_plan_t P, int64_t N, const void
   a.add(out, rows, true, true);
   st = a.check(true);
   if (st != TPCONV_OK) return st;
-  ProfScope scope(PC_NODE, 1, (cudaStream_t)stream);
+  ProfScope scope(PC_NODE, 0, (cudaStream_t)stream);
   return launch_dropout(P->dtype, P->desc, N, x, residual, drop, out, (cudaStream_t)stream) == cudaSuccess
              ? TPCONV_OK
              : TPCONV_ERR_CUDA;

@@ -11,6 +11,7 @@ enum ProfCat {
 
 int prof_open(int category, int launches, cudaStream_t s);  // slot, or -1 while profiling is off
 void prof_close(int slot, cudaStream_t s);
+void prof_count(int category, int launches);                // launches known only as they are made
 
 // Brackets one library call that launches `nk` kernels on stream s.
 struct ProfScope {

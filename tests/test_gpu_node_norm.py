@@ -392,6 +392,19 @@ def test_64_bit_offsets(torch):
     assert 0.45 < kept.float().mean().item() < 0.55
 
 
+def test_profile_counts_launches(torch):
+    from equivariant_gnn_tensor_dst_b200 import binding as B
+    p = Problem(MIXED, 5000)
+    gy, _ = p.rows()
+    B.tpconv_profile_begin(64)
+    B.tpconv_norm_forward(p.plan, p.x, p.w, p.b)                    # one launch
+    B.tpconv_norm_backward(p.plan, p.x, p.w, gy)                    # rows, reduction
+    B.tpconv_norm_backward(p.plan, p.x, p.w, gy, need_weight=False, need_bias=False)
+    B.tpconv_dropout_forward(p.plan, p.x, B.Dropout(0.1, 1))
+    ms, n = B.tpconv_profile_end()["node_features"]
+    assert n == 5 and ms > 0
+
+
 def test_binding_checks(torch):
     from equivariant_gnn_tensor_dst_b200 import binding as B
     p = Problem(MIXED, 5000)
