@@ -519,7 +519,7 @@ def _node_row(t, name, x):
     """Address of a node array like x (0: None)."""
     if t is None:
         return 0
-    if not (t.dtype is x.dtype and t.shape == x.shape and t.device == x.device and t.is_contiguous()):
+    if not (t.dtype is x.dtype and t.shape == x.shape and t.get_device() == x.get_device() and t.is_contiguous()):
         _node_bad(t, name, x.dtype, x.shape, x.device)
     return t.data_ptr()
 
@@ -528,7 +528,7 @@ def _node_vec(t, n, name, x):
     """Address of a float32 channel vector of n values on x's device (0: None)."""
     if t is None:
         return 0
-    if not (t.dtype is _torch.float32 and t.numel() == n and t.device == x.device and t.is_contiguous()):
+    if not (t.dtype is _torch.float32 and t.numel() == n and t.get_device() == x.get_device() and t.is_contiguous()):
         _node_bad(t, name, _torch.float32, (n,), x.device)
     return t.data_ptr()
 
@@ -551,7 +551,7 @@ def _node_sums(like, n, need, device):
 
 def _node_call(device, name, stream, *args):
     """One library call on the tensors' device and the given (or that device's current) stream."""
-    if device.index != _torch.cuda.current_device():
+    if device.index != _torch._C._cuda_getDevice():
         with _torch.cuda.device(device):
             return _node_call(device, name, stream, *args)
     # the handle itself: building a torch Stream object costs several microseconds

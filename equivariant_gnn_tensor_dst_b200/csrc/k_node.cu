@@ -954,6 +954,9 @@ __device__ __forceinline__ void drop_block(const NodeDesc& D, const NodeBlock& B
                     << (4 * g);
           }
         }
+        uint32_t m[V];  // all ones where a channel is kept: one AND an element
+#pragma unroll
+        for (int i = 0; i < V; ++i) m[i] = keep >> i & 1 ? ~0u : 0u;
         T* to = out + (long long)n * D.dim + first;
 #pragma unroll
         for (int k = 0; k < DC; ++k) {
@@ -963,12 +966,17 @@ __device__ __forceinline__ void drop_block(const NodeDesc& D, const NodeBlock& B
 #pragma unroll
           for (int i = 0; i < V; i += 2) {
             const int c0 = MUL_IR ? (k * V + i) / DC : i, c1 = MUL_IR ? (k * V + i + 1) / DC : i + 1;
-            float v0, v1, r0 = 0.f, r1 = 0.f;
+            float v0, v1;
             unpack<T>(wa[i / 2], v0, v1);
-            if (res) unpack<T>(wb[i / 2], r0, r1);
-            v0 = keep >> c0 & 1 ? __fmul_rn(v0, drop.scale) : 0.f;
-            v1 = keep >> c1 & 1 ? __fmul_rn(v1, drop.scale) : 0.f;
-            if (res) v0 += r0, v1 += r1;
+            const f2 t = mul2(pack2(v0, v1), both(drop.scale));
+            v0 = __uint_as_float(__float_as_uint(lo(t)) & m[c0]);
+            v1 = __uint_as_float(__float_as_uint(hi(t)) & m[c1]);
+            if (res) {
+              float r0, r1;
+              unpack<T>(wb[i / 2], r0, r1);
+              v0 += r0;
+              v1 += r1;
+            }
             o[i / 2] = pack<T>(v0, v1);
           }
           *reinterpret_cast<uint4*>(to + k * step) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -985,6 +993,7 @@ __global__ void __launch_bounds__(kThreads, kDropCtas)
   while (k + 1 < M.n && (int)blockIdx.x >= M.cta0[k + 1]) ++k;
   const NodeBlock& B = D.b[M.blk[k]];
   const uint32_t cta = blockIdx.x - M.cta0[k], ctas = M.cta0[k + 1] - M.cta0[k];
+  cudaGridDependencySynchronize();
   switch (B.d) {
     case 1: return drop_block<T, 1, false>(D, B, drop, x, res, out, N, cta, ctas);
     case 3: return drop_block<T, 3, MUL_IR>(D, B, drop, x, res, out, N, cta, ctas);
@@ -1491,11 +1500,8 @@ bool run_drop(const Call& c) {
     const long long most = (c.N + rows - 1) / rows, share = (long long)kSms * kDropCtas * B.S / c.D.dim;
     M.cta0[b + 1] = M.cta0[b] + (int)(share < 1 ? 1 : share > most ? most : share);
   }
-  const dim3 grid(M.cta0[M.n]), block(kThreads);
-  const T *x = (const T*)c.A.x, *res = (const T*)c.A.residual;
-  prof_count(PC_NODE, 1);
-  if (c.D.mul_ir) k_drop<T, true><<<grid, block, 0, c.s>>>(c.D, M, c.d, x, res, (T*)c.A.z, c.N);
-  else k_drop<T, false><<<grid, block, 0, c.s>>>(c.D, M, c.d, x, res, (T*)c.A.z, c.N);
+  launch_early(c.D.mul_ir ? k_drop<T, true> : k_drop<T, false>, M.cta0[M.n], kThreads, 0, c.s, c.D, M, c.d,
+               (const T*)c.A.x, (const T*)c.A.residual, (T*)c.A.z, c.N);
   return true;
 }
 
