@@ -910,16 +910,19 @@ TPC_NODE_KERNEL(TH, PASS_DBL, 16 / sizeof(T) * J)
 // ---- dropout alone in 16 bits, blocks whose channels come in whole packs: a thread owns V channels of
 // a row ----
 //
-// Bound by instructions (the generator's) more than by HBM.  With all 2l+1 components of its channels
+// Bound by loads' latency and the generator's instructions.  With all 2l+1 components of its channels
 // in one thread, a counter is drawn once for them and needs no exchange between lanes: 16384 x 1152
-// bf16 17 us (68 % of the copy bandwidth), 27 us by k_fwd.  Four CTAs an SM and one row a step (two
+// bf16 14 us (82 % of the copy bandwidth), 27 us by k_fwd.  Four CTAs an SM and one row a step (two
 // for scalars) measured best.  In float32 k_fwd's ring is faster (50000 x 592 with residual: 57 us, 65
 // us here).
+
+// Rows a step.
+__host__ __device__ constexpr int drop_rows(int d) { return d == 1 ? 2 : 1; }
 
 template <class T, int DC, bool MUL_IR>
 __device__ __forceinline__ void drop_block(const NodeDesc& D, const NodeBlock& B, const Drop& drop, const T* x,
                                            const T* res, T* out, uint32_t N, uint32_t cta, uint32_t ctas) {
-  constexpr int V = 16 / sizeof(T), U = DC == 1 ? 2 : 1;
+  constexpr int V = 16 / sizeof(T), U = drop_rows(DC);
   const uint32_t packs = B.C / V, lanes = packs < kThreads ? packs : kThreads, rows = kThreads / lanes;
   const uint32_t slot = threadIdx.x / lanes, lane = threadIdx.x - slot * lanes;
   if (slot >= rows) return;
@@ -1328,9 +1331,10 @@ LaunchPlan plan_launches(const Shape& sh, const NodeDesc& D, long long N) {
     } else {
       // Fewest lane-packs per row (a segment's lanes are a power of two); of equal ones the most
       // packs per lane, but 12 elements in the passes with sums and in dropout alone (fused backward
-      // 50000 x 592 f32: 104 us, 112 us with 16), and 8 in the passes with sums off the boundary, whose
-      // masks take registers (backward 50000 x 145 f32: 28 us, 31 us with 12; f16: 26 us, 29 us with 16).
-      const int lg_max = log2_lanes(L.threads, 1), few = P.edge && sums ? 8 : !P.edge && (sums || !sh.norm) ? 12 : 16;
+      // 50000 x 592 f32: 104 us, 112 us with 16), 8 in the double backward (the same rows: 105 us, 110
+      // us with 12) and in the passes with sums off the boundary, whose masks take registers (backward
+      // 50000 x 145 f32: 28 us, 31 us with 12; f16: 26 us, 29 us with 16).
+      const int lg_max = log2_lanes(L.threads, 1), few = (P.edge && sums) || sh.pass == PASS_DBL ? 8 : !P.edge && (sums || !sh.norm) ? 12 : 16;
       long long best = -1;
       for (int j = kd == KIND_WIDE ? jmax : 1; j <= jmax; ++j) {
         if (P.edge && sums && V * j > few && best >= 0) break;
@@ -1491,14 +1495,25 @@ bool run_drop(const Call& c) {
   constexpr int V = 16 / sizeof(T);
   for (int b = 0; b < c.D.n_blocks; ++b)
     if (c.D.b[b].C % V != 0) return false;
+  // CTAs in proportion to what the blocks' steps take: a load's latency and the packs.  The latency as 8
+  // packs, 2 with a residual (twice the loads on the way): 16384 x 1152 bf16 14.1 us, 15.3 us with 2
+  // (16.9 us by bytes alone); 50000 x 592 bf16 with residual 33.4 us, 36.0 us with 8.
   RowMap M{};
   M.n = c.D.n_blocks;
+  long long work[MAX_BLOCKS], most[MAX_BLOCKS], total = 0;
   for (int b = 0; b < M.n; ++b) {
     const NodeBlock& B = c.D.b[b];
+    const long long packs = B.C / V, lanes = packs < kThreads ? packs : kThreads;
+    const long long rows = kThreads / lanes * drop_rows(B.d);
+    most[b] = (c.N + rows - 1) / rows;
+    const int loads = drop_rows(B.d) * B.d * (c.A.residual ? 2 : 1);
+    work[b] = most[b] * ((packs + lanes - 1) / lanes) * ((c.A.residual ? 2 : 8) + loads);
+    total += work[b];
+  }
+  for (int b = 0; b < M.n; ++b) {
+    const long long share = work[b] * kSms * kDropCtas / total;
     M.blk[b] = b;
-    const long long packs = B.C / V, rows = packs < kThreads ? kThreads / packs : 1;
-    const long long most = (c.N + rows - 1) / rows, share = (long long)kSms * kDropCtas * B.S / c.D.dim;
-    M.cta0[b + 1] = M.cta0[b] + (int)(share < 1 ? 1 : share > most ? most : share);
+    M.cta0[b + 1] = M.cta0[b] + (int)(share < 1 ? 1 : share > most[b] ? most[b] : share);
   }
   launch_early(c.D.mul_ir ? k_drop<T, true> : k_drop<T, false>, M.cta0[M.n], kThreads, 0, c.s, c.D, M, c.d,
                (const T*)c.A.x, (const T*)c.A.residual, (T*)c.A.z, c.N);
