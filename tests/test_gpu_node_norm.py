@@ -141,11 +141,12 @@ def test_degenerate_rows(torch):
     assert torch.isfinite(gx[1]).all() and torch.isfinite(gx[2, :16]).all()
 
 
-def test_optional_arguments(torch):
+@pytest.mark.parametrize("irreps,n", [(MIXED, 50), (MIXED, 3000), (ODD, 700), ("4096x0e", 300), ("20001x0e", 3)])
+def test_optional_arguments(torch, irreps, n):
     """No weight and bias are ones and zeros; missing tangents are zeros; outputs are computed one
     by one as together."""
     from equivariant_gnn_tensor_dst_b200 import binding as B
-    p = Problem(MIXED, 50)
+    p = Problem(irreps, n)
     one, zero = torch.ones_like(p.w), torch.zeros_like(p.b)
     assert torch.equal(B.tpconv_norm_forward(p.plan, p.x), B.tpconv_norm_forward(p.plan, p.x, one, zero))
     gy, _ = p.rows()
@@ -372,17 +373,21 @@ def test_guard_bands(torch):
                     assert bool((t[:pad] == 9.0).all()) and bool((t[pad + size:] == 9.0).all())
 
 
-def test_64_bit_offsets(torch):
-    """Rows beyond 2^31 elements (16 bits: 4.4 GB an array): the last rows equal the same rows alone."""
+@pytest.mark.parametrize("irreps,dtype", [("2048x0e", "bfloat16"), ("2047x0e", "float16")])
+def test_64_bit_offsets(torch, irreps, dtype):
+    """Rows beyond 2^31 elements (16 bits: 4.4 GB an array), on the 16-byte boundary and off it: the
+    last rows equal the same rows alone."""
     from equivariant_gnn_tensor_dst_b200 import binding as B
-    irreps, dim = "2048x0e", 2048
-    n = (1 << 31) // dim + 40
-    plan = B.NodePlan(irreps, torch.bfloat16)
-    x = torch.randn(64, dim, device="cuda").to(torch.bfloat16).repeat(n // 64 + 1, 1)[:n].contiguous()
+    T = getattr(torch, dtype)
+    plan = B.NodePlan(irreps, T)
+    dim = plan.dim
+    n = (1 << 31) // dim + 80
+    x = torch.randn(64, dim, device="cuda").to(T).repeat(n // 64 + 1, 1)[:n].contiguous()
     gy = x.flip(1).contiguous()
     y = B.tpconv_norm_forward(plan, x)
     gx = B.tpconv_norm_backward(plan, x, None, gy, need_weight=False, need_bias=False)[0]
-    tail = n - 40
+    tail = (n - 40) // 8 * 8         # the same number modulo 8
+    assert tail * dim > 1 << 31
     assert torch.equal(y[tail:], B.tpconv_norm_forward(plan, x[tail:].clone()))
     assert torch.equal(gx[tail:], B.tpconv_norm_backward(plan, x[tail:].clone(), None, gy[tail:].clone())[0])
     d = B.Dropout(0.5, 3)
