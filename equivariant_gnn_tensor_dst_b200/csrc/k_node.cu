@@ -518,6 +518,12 @@ __device__ __forceinline__ void apply_mask(f2 (&v)[P], uint32_t keep, float scal
   }
 }
 
+// Whether the sum of squares about the mean, taken as a difference (sum of squares less mean times
+// sum), has to be taken again around the mean: the difference is exact to a few 2^-24 of itself while
+// the mean is at most twice the spread.  Also where it is no number.  All warps of a group have read the
+// same values and added them in the same order, so all take the same way (and meet at its barrier).
+__device__ __forceinline__ bool large_mean(float mu, float S, float q) { return !(mu * mu * S <= 4.f * q); }
+
 // v + m at the lane's elements inside the segment (the others hold zeros)
 template <int V, int J, bool EDGE>
 __device__ __forceinline__ void shift_by(f2 (&v)[V * J / 2], float m, uint32_t valid) {
@@ -608,16 +614,33 @@ TPC_NODE_KERNEL(TH, PASS_FWD, 16 / sizeof(T) * J)
       z.next();
     }
     if constexpr (NORM) {
+      float q[1];
+      bool second = true;
       if (centred) {
-        float mu[1] = {total(v)};
-        at.sum(mu);
-        shift_by<V, J, EDGE>(v, -mu[0] * inv, valid);
-      }
-      f2 q2 = mul2(v[0], v[0]);
+        float mu;
+        if (at.G > 32) {  // one exchange between the warps instead of two: see k_bwd
+          f2 vv = mul2(v[0], v[0]);
 #pragma unroll
-      for (int p = 1; p < P; ++p) q2 = fma2(v[p], v[p], q2);
-      float q[1] = {lo(q2) + hi(q2)};
-      at.sum(q);
+          for (int p = 1; p < P; ++p) vv = fma2(v[p], v[p], vv);
+          float m[2] = {total(v), lo(vv) + hi(vv)};
+          at.sum(m);
+          mu = m[0] * inv;
+          q[0] = m[1] - m[0] * mu;
+          second = large_mean(mu, (float)B.S, q[0]);
+        } else {
+          float m[1] = {total(v)};
+          at.sum(m);
+          mu = m[0] * inv;
+        }
+        shift_by<V, J, EDGE>(v, -mu, valid);
+      }
+      if (second) {
+        f2 q2 = mul2(v[0], v[0]);
+#pragma unroll
+        for (int p = 1; p < P; ++p) q2 = fma2(v[p], v[p], q2);
+        q[0] = lo(q2) + hi(q2);
+        at.sum(q);
+      }
       const f2 r = both(rsqrtf(q[0] * inv + D.eps));
 #pragma unroll
       for (int p = 0; p < P; ++p) v[p] = fma2(mul2(v[p], r), w[p], b[p]);
@@ -734,9 +757,7 @@ TPC_NODE_KERNEL(TH, PASS_BWD, 16 / sizeof(T) * J)
     bool second = true;
     if (centred) {
       // Groups of several warps wait for one another in a sum: theirs has the second moments as well
-      // (4096x0e bf16: 54 us, 57 us with two sums), which are exact enough, a few 2^-24 of the spread,
-      // unless the mean is large.  All warps of a group read the same values and add them in the same
-      // order, so all take the same way.
+      // (4096x0e bf16: 54 us, 57 us with two sums; forward 29 us, 33 us).
       const bool once = at.G > 32;
       f2 t[P], uu = mul2(u[0], u[0]), ut = mul2(u[0], product(0));
 #pragma unroll
@@ -754,7 +775,7 @@ TPC_NODE_KERNEL(TH, PASS_BWD, 16 / sizeof(T) * J)
         ma = m[1] * inv;
         q[0] = m[2] - m[0] * mu;
         q[1] = m[3] - m[1] * mu;
-        second = !(mu * mu * (float)B.S <= 4.f * q[0]);
+        second = large_mean(mu, (float)B.S, q[0]);
       } else {
         float m[2] = {total(u), total(t)};
         at.sum(m);

@@ -75,16 +75,21 @@ def test_rows_beyond_one_launch_range():
     _all_passes(Problem("4x0e", 70001))
 
 
-def test_large_offset():
-    """A mean a thousand times the spread: the spread is taken around the mean, not as a
-    difference of squares."""
+@pytest.mark.parametrize("irreps", ["96x0e", "1024x0e", "4096x0e", "1999x0e"])
+def test_large_offset(irreps):
+    """A mean a thousand times the spread in some rows: the spread is taken around the mean, not as a
+    difference of squares; in groups of lanes and of several warps."""
     from equivariant_gnn_tensor_dst_b200 import binding
-    p = Problem("96x0e", 50, offset=1000.0)
+    p = Problem(irreps, 400)
+    p.x[some_rows(400)] += 1000.0
+    x64 = p.x.double().cpu().numpy()
     y = binding.tpconv_norm_forward(p.plan, p.x, p.w, p.b).double().cpu().numpy()
-    ref = node.norm_forward(p.R, p.x64, p.w64, p.b64)
-    # an error of 2^-24 of the mean (1000, of rows with spread e^-1.5 .. e^1.5) in every u, and the
-    # mean's own sum, 20 additions deep at most
-    assert np.abs(y - ref).max() <= 40 * 2.0 ** -24 * 1000 / np.exp(-1.5) * 2
+    ref = node.norm_forward(p.R, x64, p.w64, p.b64)
+    # an error of the mean, 2^-24 (S / 32 + 16) of |x|, in every u, through r; rows scaled by their spread
+    spread = np.std(x64, axis=1, keepdims=True)
+    err = 2.0 ** -24 * (p.R.dim / 32 + 24) * np.abs(x64).mean(axis=1, keepdims=True) / spread
+    h = np.abs(x64 - x64.mean(axis=1, keepdims=True)) / spread
+    assert np.all(np.abs(y - ref) <= 2 * (1 + h) * (err + tol32(p.R)) * np.abs(p.w64).max() + tol32(p.R))
 
 
 def some_rows(n):
