@@ -6,6 +6,7 @@ allocate outputs and workspaces and to name the current CUDA stream.  If the sha
 library is missing the import of ``lib()`` fails loudly; there is no fallback.
 """
 
+import contextlib
 import ctypes
 import os
 
@@ -220,6 +221,20 @@ def _need(t, dtype, name):
         raise ValueError(f"{name} must be contiguous")
 
 
+_CURRENT = contextlib.nullcontext()
+
+
+def _on(stream):
+    """Where a call makes its own tensors: on the stream that its kernels run on (None: the current one).
+    The allocator gives a block away again in the order of its stream, so a workspace that is dropped
+    when the call returns, its kernels still queued, is safe there, and a new block has no work of
+    another stream pending."""
+    if stream is None:
+        return _CURRENT
+    import torch
+    return torch.cuda.stream(stream)
+
+
 def workspace(nbytes, device):
     import torch
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
@@ -399,6 +414,11 @@ def tpconv_gather_rows(a, perm, stream=None):
 
 # ---------------------------------------------------------------------------
 # node-feature operators (include/tpconv_node.h)
+#
+# A call with stream= makes its outputs and its workspace on that stream, as calls inside
+# torch.cuda.stream(stream) do: inputs have to be ready there, and outputs that are used on another
+# stream follow torch's rule for such tensors (wait for the stream; Tensor.record_stream before the
+# tensor is dropped).
 # ---------------------------------------------------------------------------
 
 _torch = None   # torch, once a NodePlan exists (an import statement in every call costs)
@@ -562,7 +582,8 @@ def _node_call(device, name, stream, *args):
 
 
 def _node_ws(plan, N, ws, device):
-    """(workspace kept alive, address, bytes)"""
+    """(workspace, address, bytes); a new one belongs to the stream that it is made on, and its owner may drop it
+    once the kernels that use it are queued there"""
     if ws is None:
         ws = workspace(plan.workspace_bytes(N), device)
     elif ws.device != device or not ws.is_contiguous():
@@ -574,7 +595,8 @@ def tpconv_norm_forward(plan, x, weight=None, bias=None, out=None, stream=None):
     """Irreps layer norm of node rows x [N, dim]; weight [channels], bias [biases] float32."""
     px = _node_x(plan, x, "x")
     pw, pb = _node_vec(weight, plan.channels, "weight", x), _node_vec(bias, plan.biases, "bias", x)
-    out, po = _node_new(x, True) if out is None else (out, _node_row(out, "out", x))
+    with _on(stream):
+        out, po = _node_new(x, True) if out is None else (out, _node_row(out, "out", x))
     _node_call(x.device, "tpconv_norm_forward", stream, plan._h, x.shape[0], px, pw, pb, po)
     return out
 
@@ -584,15 +606,16 @@ def tpconv_norm_backward(plan, x, weight, grad_y, need_x=True, need_weight=True,
     """Returns (grad_x [N, dim], grad_weight [channels], grad_bias [biases])."""
     dev, N, C, Cb = x.device, x.shape[0], plan.channels, plan.biases
     px, pg, pw = _node_x(plan, x, "x"), _node_row(grad_y, "grad_y", x), _node_vec(weight, C, "weight", x)
-    if outputs is None:
-        gx, pgx = _node_new(x, need_x)
-        gw, pgw = _node_sums(weight, C, need_weight, dev)
-        gb, pgb = _node_sums(None, Cb, need_bias, dev)
-    else:
-        gx, gw, gb = outputs
-        pgx = _node_row(gx, "grad_x", x)
-        pgw, pgb = _node_vec(gw, C, "grad_weight", x), _node_vec(gb, Cb, "grad_bias", x)
-    ws, pws, nws = _node_ws(plan, N, ws, dev)
+    with _on(stream):
+        if outputs is None:
+            gx, pgx = _node_new(x, need_x)
+            gw, pgw = _node_sums(weight, C, need_weight, dev)
+            gb, pgb = _node_sums(None, Cb, need_bias, dev)
+        else:
+            gx, gw, gb = outputs
+            pgx = _node_row(gx, "grad_x", x)
+            pgw, pgb = _node_vec(gw, C, "grad_weight", x), _node_vec(gb, Cb, "grad_bias", x)
+        ws, pws, nws = _node_ws(plan, N, ws, dev)
     _node_call(dev, "tpconv_norm_backward", stream, plan._h, N, px, pw, pg, pgx, pgw, pgb, pws, nws)
     return gx, gw, gb
 
@@ -604,15 +627,16 @@ def tpconv_norm_double_backward(plan, x, weight, grad_y, gg_x=None, gg_weight=No
     px, pg, pp = _node_x(plan, x, "x"), _node_row(grad_y, "grad_y", x), _node_row(gg_x, "gg_x", x)
     pw, pt = _node_vec(weight, C, "weight", x), _node_vec(gg_weight, C, "gg_weight", x)
     ptb = _node_vec(gg_bias, plan.biases, "gg_bias", x)
-    if outputs is None:
-        gx, pgx = _node_new(x, need_x)
-        gw, pgw = _node_sums(weight, C, need_weight, dev)
-        gg, pgg = _node_new(x, need_grad_y)
-    else:
-        gx, gw, gg = outputs
-        pgx, pgg = _node_row(gx, "grad_x", x), _node_row(gg, "grad_grad_y", x)
-        pgw = _node_vec(gw, C, "grad_weight", x)
-    ws, pws, nws = _node_ws(plan, N, ws, dev)
+    with _on(stream):
+        if outputs is None:
+            gx, pgx = _node_new(x, need_x)
+            gw, pgw = _node_sums(weight, C, need_weight, dev)
+            gg, pgg = _node_new(x, need_grad_y)
+        else:
+            gx, gw, gg = outputs
+            pgx, pgg = _node_row(gx, "grad_x", x), _node_row(gg, "grad_grad_y", x)
+            pgw = _node_vec(gw, C, "grad_weight", x)
+        ws, pws, nws = _node_ws(plan, N, ws, dev)
     _node_call(dev, "tpconv_norm_double_backward", stream, plan._h, N, px, pw, pg, pp, pt, ptb, pgx, pgw, pgg, pws,
                nws)
     return gx, gw, gg
@@ -621,7 +645,8 @@ def tpconv_norm_double_backward(plan, x, weight, grad_y, gg_x=None, gg_weight=No
 def tpconv_dropout_forward(plan, x, dropout, residual=None, out=None, stream=None):
     """residual + dropout(x); ``dropout`` is a Dropout.  out may be x or residual (in place)."""
     px, pr = _node_x(plan, x, "x"), _node_row(residual, "residual", x)
-    out, po = _node_new(x, True) if out is None else (out, _node_row(out, "out", x))
+    with _on(stream):
+        out, po = _node_new(x, True) if out is None else (out, _node_row(out, "out", x))
     _node_call(x.device, "tpconv_dropout_forward", stream, plan._h, x.shape[0], px, pr, dropout.spec(x.device), po)
     return out
 
@@ -629,7 +654,8 @@ def tpconv_dropout_forward(plan, x, dropout, residual=None, out=None, stream=Non
 def tpconv_dropout_backward(plan, grad_out, dropout, out=None, stream=None):
     """grad_x of tpconv_dropout_forward (the residual's gradient is grad_out itself)."""
     pg = _node_x(plan, grad_out, "grad_out")
-    out, po = _node_new(grad_out, True) if out is None else (out, _node_row(out, "out", grad_out))
+    with _on(stream):
+        out, po = _node_new(grad_out, True) if out is None else (out, _node_row(out, "out", grad_out))
     _node_call(grad_out.device, "tpconv_dropout_backward", stream, plan._h, grad_out.shape[0], pg,
                dropout.spec(grad_out.device), po)
     return out
@@ -639,11 +665,12 @@ def tpconv_dropout_norm_forward(plan, x, dropout, residual=None, weight=None, bi
     """Returns (z, y): z = residual + dropout(x), y = norm(z)."""
     px, pr = _node_x(plan, x, "x"), _node_row(residual, "residual", x)
     pw, pb = _node_vec(weight, plan.channels, "weight", x), _node_vec(bias, plan.biases, "bias", x)
-    if outputs is None:
-        (z, pz), (y, py) = _node_new(x, True), _node_new(x, True)
-    else:
-        z, y = outputs
-        pz, py = _node_row(z, "z", x), _node_row(y, "y", x)
+    with _on(stream):
+        if outputs is None:
+            (z, pz), (y, py) = _node_new(x, True), _node_new(x, True)
+        else:
+            z, y = outputs
+            pz, py = _node_row(z, "z", x), _node_row(y, "y", x)
     _node_call(x.device, "tpconv_dropout_norm_forward", stream, plan._h, x.shape[0], px, pr, dropout.spec(x.device),
                pw, pb, pz, py)
     return z, y
@@ -655,16 +682,17 @@ def tpconv_dropout_norm_backward(plan, z, weight, grad_y, dropout, grad_z=None, 
     dev, N, C, Cb = z.device, z.shape[0], plan.channels, plan.biases
     pz, pg, pgz = _node_x(plan, z, "z"), _node_row(grad_y, "grad_y", z), _node_row(grad_z, "grad_z", z)
     pw = _node_vec(weight, C, "weight", z)
-    if outputs is None:
-        gx, pgx = _node_new(z, need_x)
-        gr, pgr = _node_new(z, need_residual)
-        gw, pgw = _node_sums(weight, C, need_weight, dev)
-        gb, pgb = _node_sums(None, Cb, need_bias, dev)
-    else:
-        gx, gr, gw, gb = outputs
-        pgx, pgr = _node_row(gx, "grad_x", z), _node_row(gr, "grad_residual", z)
-        pgw, pgb = _node_vec(gw, C, "grad_weight", z), _node_vec(gb, Cb, "grad_bias", z)
-    ws, pws, nws = _node_ws(plan, N, ws, dev)
+    with _on(stream):
+        if outputs is None:
+            gx, pgx = _node_new(z, need_x)
+            gr, pgr = _node_new(z, need_residual)
+            gw, pgw = _node_sums(weight, C, need_weight, dev)
+            gb, pgb = _node_sums(None, Cb, need_bias, dev)
+        else:
+            gx, gr, gw, gb = outputs
+            pgx, pgr = _node_row(gx, "grad_x", z), _node_row(gr, "grad_residual", z)
+            pgw, pgb = _node_vec(gw, C, "grad_weight", z), _node_vec(gb, Cb, "grad_bias", z)
+        ws, pws, nws = _node_ws(plan, N, ws, dev)
     _node_call(dev, "tpconv_dropout_norm_backward", stream, plan._h, N, pz, pw, pg, pgz, dropout.spec(dev), pgx, pgr,
                pgw, pgb, pws, nws)
     return gx, gr, gw, gb
