@@ -197,6 +197,11 @@ class Plan:
 
 # ---------------------------------------------------------------------------
 # torch-facing calls
+#
+# A call with stream= makes its outputs and its workspace on that stream, as calls inside
+# torch.cuda.stream(stream) do: inputs have to be ready there, and outputs that are used on another
+# stream follow torch's rule for such tensors (wait for the stream; Tensor.record_stream before the
+# tensor is dropped).
 # ---------------------------------------------------------------------------
 
 def _ptr(t):
@@ -246,12 +251,13 @@ def tpconv_csr_transpose(row_ptr, src, n_nodes, stream=None):
     _need(src, torch.int32, "src")
     E = src.numel()
     dev = row_ptr.device
-    t_ptr = torch.empty(n_nodes + 1, dtype=torch.int32, device=dev)
-    t_eid = torch.empty(max(E, 1), dtype=torch.int32, device=dev)
-    t_dst = torch.empty(max(E, 1), dtype=torch.int32, device=dev)
     nb = ctypes.c_size_t()
     check(lib().tpconv_csr_transpose_workspace_bytes(n_nodes, E, ctypes.byref(nb)))
-    ws = workspace(nb.value, dev)
+    with _on(stream):
+        t_ptr = torch.empty(n_nodes + 1, dtype=torch.int32, device=dev)
+        t_eid = torch.empty(max(E, 1), dtype=torch.int32, device=dev)
+        t_dst = torch.empty(max(E, 1), dtype=torch.int32, device=dev)
+        ws = workspace(nb.value, dev)
     check(lib().tpconv_csr_transpose(n_nodes, E, _ptr(row_ptr), _ptr(src), _ptr(t_ptr), _ptr(t_eid),
                                      _ptr(t_dst), _ptr(ws), ws.numel(), _stream(stream)),
           "tpconv_csr_transpose")
@@ -260,7 +266,8 @@ def tpconv_csr_transpose(row_ptr, src, n_nodes, stream=None):
 
 def tpconv_validate_graph(row_ptr, src, n_nodes, stream=None):
     import torch
-    err = torch.zeros(4, dtype=torch.int32, device=row_ptr.device)
+    with _on(stream):
+        err = torch.zeros(4, dtype=torch.int32, device=row_ptr.device)
     check(lib().tpconv_validate_graph(n_nodes, src.numel(), _ptr(row_ptr), _ptr(src), _ptr(err),
                                       _stream(stream)), "tpconv_validate_graph")
     return err[:1]
@@ -273,10 +280,11 @@ def tpconv_forward(plan, x, pos, row_ptr, src, W, out=None, ws=None, stream=None
     _need(row_ptr, torch.int32, "row_ptr")
     _need(src, torch.int32, "src")
     N, E = pos.shape[0], src.numel()
-    if out is None:
-        out = torch.empty(N, plan.dim_out, dtype=torch.float32, device=x.device)
-    if ws is None:
-        ws = workspace(plan.workspace_bytes(N, E, PASS_FORWARD), x.device)
+    with _on(stream):
+        if out is None:
+            out = torch.empty(N, plan.dim_out, dtype=torch.float32, device=x.device)
+        if ws is None:
+            ws = workspace(plan.workspace_bytes(N, E, PASS_FORWARD), x.device)
     check(lib().tpconv_forward(plan.handle, N, E, _ptr(x), _ptr(pos), _ptr(row_ptr), _ptr(src), _ptr(W),
                                _ptr(out), _ptr(ws), ws.numel(), _stream(stream)), "tpconv_forward")
     return out
@@ -287,14 +295,15 @@ def tpconv_backward(plan, x, pos, row_ptr, src, t_ptr, t_eid, t_dst, W, grad_out
     import torch
     N, E = pos.shape[0], src.numel()
     dev = x.device
-    if outputs is None:
-        gx = torch.empty(N, plan.dim_in, dtype=torch.float32, device=dev) if need_x else None
-        gp = torch.empty(N, 3, dtype=torch.float32, device=dev) if need_pos else None
-        gw = torch.empty(plan.num_basis, plan.weight_cols, dtype=torch.float32, device=dev) if need_W else None
-    else:
-        gx, gp, gw = outputs
-    if ws is None:
-        ws = workspace(plan.workspace_bytes(N, E, PASS_BACKWARD), dev)
+    with _on(stream):
+        if outputs is None:
+            gx = torch.empty(N, plan.dim_in, dtype=torch.float32, device=dev) if need_x else None
+            gp = torch.empty(N, 3, dtype=torch.float32, device=dev) if need_pos else None
+            gw = torch.empty(plan.num_basis, plan.weight_cols, dtype=torch.float32, device=dev) if need_W else None
+        else:
+            gx, gp, gw = outputs
+        if ws is None:
+            ws = workspace(plan.workspace_bytes(N, E, PASS_BACKWARD), dev)
     check(lib().tpconv_backward(plan.handle, N, E, _ptr(x), _ptr(pos), _ptr(row_ptr), _ptr(src),
                                 _ptr(t_ptr), _ptr(t_eid), _ptr(t_dst), _ptr(W), _ptr(grad_out),
                                 _ptr(gx), _ptr(gp), _ptr(gw), _ptr(ws), ws.numel(), _stream(stream)),
@@ -310,10 +319,11 @@ def tpconv_forward_embedded(plan, x, Y, phi, row_ptr, src, W, out=None, ws=None,
     _need(row_ptr, torch.int32, "row_ptr")
     _need(src, torch.int32, "src")
     N, E = row_ptr.numel() - 1, src.numel()
-    if out is None:
-        out = torch.empty(N, plan.dim_out, dtype=torch.float32, device=x.device)
-    if ws is None:
-        ws = workspace(plan.workspace_bytes(N, E, PASS_FORWARD), x.device)
+    with _on(stream):
+        if out is None:
+            out = torch.empty(N, plan.dim_out, dtype=torch.float32, device=x.device)
+        if ws is None:
+            ws = workspace(plan.workspace_bytes(N, E, PASS_FORWARD), x.device)
     check(lib().tpconv_forward_embedded(plan.handle, N, E, _ptr(x), _ptr(Y), _ptr(phi), _ptr(row_ptr), _ptr(src),
                                         _ptr(W), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)),
           "tpconv_forward_embedded")
@@ -326,15 +336,16 @@ def tpconv_backward_embedded(plan, x, Y, phi, row_ptr, src, t_ptr, t_eid, t_dst,
     import torch
     N, E = row_ptr.numel() - 1, src.numel()
     dev = x.device
-    if outputs is None:
-        gx = torch.empty(N, plan.dim_in, dtype=torch.float32, device=dev) if need_x else None
-        gw = torch.empty(plan.num_basis, plan.weight_cols, dtype=torch.float32, device=dev) if need_W else None
-        gphi = torch.empty(E, plan.num_basis, dtype=torch.float32, device=dev) if need_phi else None
-        gY = torch.empty(E, Y.shape[1], dtype=torch.float32, device=dev) if need_Y else None
-    else:
-        gx, gw, gphi, gY = outputs
-    if ws is None:
-        ws = workspace(plan.workspace_bytes(N, E, PASS_BACKWARD), dev)
+    with _on(stream):
+        if outputs is None:
+            gx = torch.empty(N, plan.dim_in, dtype=torch.float32, device=dev) if need_x else None
+            gw = torch.empty(plan.num_basis, plan.weight_cols, dtype=torch.float32, device=dev) if need_W else None
+            gphi = torch.empty(E, plan.num_basis, dtype=torch.float32, device=dev) if need_phi else None
+            gY = torch.empty(E, Y.shape[1], dtype=torch.float32, device=dev) if need_Y else None
+        else:
+            gx, gw, gphi, gY = outputs
+        if ws is None:
+            ws = workspace(plan.workspace_bytes(N, E, PASS_BACKWARD), dev)
     check(lib().tpconv_backward_embedded(plan.handle, N, E, _ptr(x), _ptr(Y), _ptr(phi), _ptr(row_ptr), _ptr(src),
                                          _ptr(t_ptr), _ptr(t_eid), _ptr(t_dst), _ptr(W), _ptr(grad_out),
                                          _ptr(gx), _ptr(gw), _ptr(gphi), _ptr(gY), _ptr(ws), ws.numel(),
@@ -351,17 +362,18 @@ def tpconv_double_backward(plan, x, pos, row_ptr, src, t_ptr, t_eid, t_dst, W, g
     import torch
     N, E = pos.shape[0], src.numel()
     dev = x.device
-    if outputs is None:
-        gx = torch.empty(N, plan.dim_in, dtype=torch.float32, device=dev) if need_x else None
-        gw = torch.empty(plan.num_basis, plan.weight_cols, dtype=torch.float32, device=dev) if need_W else None
-        gg = torch.empty(N, plan.dim_out, dtype=torch.float32, device=dev) if need_grad_out else None
-        gp = torch.empty(N, 3, dtype=torch.float32, device=dev) if need_pos else None
-    elif need_pos:
-        gx, gw, gg, gp = outputs
-    else:
-        (gx, gw, gg), gp = outputs, None
-    if ws is None:
-        ws = workspace(plan.workspace_bytes(N, E, PASS_DOUBLE_BACKWARD), dev)
+    with _on(stream):
+        if outputs is None:
+            gx = torch.empty(N, plan.dim_in, dtype=torch.float32, device=dev) if need_x else None
+            gw = torch.empty(plan.num_basis, plan.weight_cols, dtype=torch.float32, device=dev) if need_W else None
+            gg = torch.empty(N, plan.dim_out, dtype=torch.float32, device=dev) if need_grad_out else None
+            gp = torch.empty(N, 3, dtype=torch.float32, device=dev) if need_pos else None
+        elif need_pos:
+            gx, gw, gg, gp = outputs
+        else:
+            (gx, gw, gg), gp = outputs, None
+        if ws is None:
+            ws = workspace(plan.workspace_bytes(N, E, PASS_DOUBLE_BACKWARD), dev)
     check(lib().tpconv_double_backward(plan.handle, N, E, _ptr(x), _ptr(pos), _ptr(row_ptr), _ptr(src),
                                        _ptr(t_ptr), _ptr(t_eid), _ptr(t_dst), _ptr(W), _ptr(grad_out),
                                        _ptr(gg_x), _ptr(gg_pos), _ptr(gg_W), _ptr(gx), _ptr(gw), _ptr(gg),
@@ -375,10 +387,11 @@ def tpconv_spatial_order(pos, stream=None):
     import torch
     _need(pos, torch.float32, "pos")
     N = pos.shape[0]
-    perm = torch.empty(max(N, 1), dtype=torch.int32, device=pos.device)
     nb = ctypes.c_size_t()
     check(lib().tpconv_spatial_order_workspace_bytes(N, ctypes.byref(nb)), "tpconv_spatial_order_workspace_bytes")
-    ws = workspace(nb.value, pos.device)
+    with _on(stream):
+        perm = torch.empty(max(N, 1), dtype=torch.int32, device=pos.device)
+        ws = workspace(nb.value, pos.device)
     check(lib().tpconv_spatial_order(N, _ptr(pos), _ptr(perm), _ptr(ws), ws.numel(), _stream(stream)),
           "tpconv_spatial_order")
     return perm[:N]
@@ -392,9 +405,10 @@ def tpconv_permute_graph(row_ptr, src, perm, stream=None):
     _need(perm, torch.int32, "perm")
     N, E = row_ptr.numel() - 1, src.numel()
     dev = row_ptr.device
-    rp = torch.empty(N + 1, dtype=torch.int32, device=dev)
-    so = torch.empty(max(E, 1), dtype=torch.int32, device=dev)
-    inv = torch.empty(max(N, 1), dtype=torch.int32, device=dev)
+    with _on(stream):
+        rp = torch.empty(N + 1, dtype=torch.int32, device=dev)
+        so = torch.empty(max(E, 1), dtype=torch.int32, device=dev)
+        inv = torch.empty(max(N, 1), dtype=torch.int32, device=dev)
     check(lib().tpconv_permute_graph(N, E, _ptr(row_ptr), _ptr(src), _ptr(perm), _ptr(rp), _ptr(so), _ptr(inv),
                                      _stream(stream)), "tpconv_permute_graph")
     return rp, so[:E], inv[:N]
@@ -406,7 +420,8 @@ def tpconv_gather_rows(a, perm, stream=None):
     _need(a, torch.float32, "a")
     _need(perm, torch.int32, "perm")
     rows, width = a.shape[0], (a.numel() // a.shape[0] if a.shape[0] else 0)
-    out = torch.empty_like(a)
+    with _on(stream):
+        out = torch.empty_like(a)
     check(lib().tpconv_gather_rows(perm.numel(), width, _ptr(a), _ptr(perm), _ptr(out), _stream(stream)),
           "tpconv_gather_rows")
     return out
@@ -414,11 +429,6 @@ def tpconv_gather_rows(a, perm, stream=None):
 
 # ---------------------------------------------------------------------------
 # node-feature operators (include/tpconv_node.h)
-#
-# A call with stream= makes its outputs and its workspace on that stream, as calls inside
-# torch.cuda.stream(stream) do: inputs have to be ready there, and outputs that are used on another
-# stream follow torch's rule for such tensors (wait for the stream; Tensor.record_stream before the
-# tensor is dropped).
 # ---------------------------------------------------------------------------
 
 _torch = None   # torch, once a NodePlan exists (an import statement in every call costs)

@@ -74,3 +74,60 @@ def test_node_tensors_belong_to_the_stream(node, made, name):
         assert made and all(s is stream for s, _ in made), made
     if name.endswith("backward") and name != "dropout_backward":
         assert (None, max(plan.workspace_bytes(3000), 256)) in made
+
+
+class Library:
+    """The library's host functions; compute calls are recorded by their stream (the last argument)."""
+
+    def __init__(self, real, streams):
+        self.real, self.streams = real, streams
+
+    def __getattr__(self, name):
+        if name.endswith("_workspace_bytes") or name.startswith("tpconv_plan"):
+            return getattr(self.real, name)
+        return lambda *args: self.streams.append(args[-1]) or 0
+
+
+@pytest.fixture
+def graph(monkeypatch, made):
+    streams = []
+    plan = B.Plan("4x0e+4x1o", 1, "4x0e+4x1o")
+    library = Library(B.lib(), streams)
+    monkeypatch.setattr(B, "lib", lambda: library)
+    monkeypatch.setattr(B, "_need", lambda t, dtype, name: None)
+    monkeypatch.setattr(B, "_stream", lambda stream: stream)
+    n, e = 50, 400
+    i32 = lambda *v: torch.ones(*v, dtype=torch.int32)
+    a = dict(x=torch.ones(n, plan.dim_in), pos=torch.ones(n, 3), row_ptr=i32(n + 1), src=i32(e), t_ptr=i32(n + 1),
+             t_eid=i32(e), t_dst=i32(e), W=torch.ones(plan.num_basis, plan.weight_cols), g=torch.ones(n, plan.dim_out),
+             Y=torch.ones(e, 4), phi=torch.ones(e, plan.num_basis), perm=i32(n), n=n)
+    return plan, a, streams
+
+
+GRAPH_CALLS = {
+    "csr_transpose": lambda p, a, **k: B.tpconv_csr_transpose(a["row_ptr"], a["src"], a["n"], **k),
+    "validate_graph": lambda p, a, **k: B.tpconv_validate_graph(a["row_ptr"], a["src"], a["n"], **k),
+    "forward": lambda p, a, **k: B.tpconv_forward(p, a["x"], a["pos"], a["row_ptr"], a["src"], a["W"], **k),
+    "backward": lambda p, a, **k: B.tpconv_backward(
+        p, a["x"], a["pos"], a["row_ptr"], a["src"], a["t_ptr"], a["t_eid"], a["t_dst"], a["W"], a["g"], **k),
+    "forward_embedded": lambda p, a, **k: B.tpconv_forward_embedded(
+        p, a["x"], a["Y"], a["phi"], a["row_ptr"], a["src"], a["W"], **k),
+    "backward_embedded": lambda p, a, **k: B.tpconv_backward_embedded(
+        p, a["x"], a["Y"], a["phi"], a["row_ptr"], a["src"], a["t_ptr"], a["t_eid"], a["t_dst"], a["W"], a["g"], **k),
+    "double_backward": lambda p, a, **k: B.tpconv_double_backward(
+        p, a["x"], a["pos"], a["row_ptr"], a["src"], a["t_ptr"], a["t_eid"], a["t_dst"], a["W"], a["g"],
+        gg_x=a["x"], need_pos=True, **k),
+    "spatial_order": lambda p, a, **k: B.tpconv_spatial_order(a["pos"], **k),
+    "permute_graph": lambda p, a, **k: B.tpconv_permute_graph(a["row_ptr"], a["src"], a["perm"], **k),
+    "gather_rows": lambda p, a, **k: B.tpconv_gather_rows(a["x"], a["perm"], **k),
+}
+
+
+@pytest.mark.parametrize("name", sorted(GRAPH_CALLS))
+def test_convolution_and_graph_tensors_belong_to_the_stream(graph, made, name):
+    plan, a, streams = graph
+    for stream in (Side(), None):
+        del made[:], streams[:]
+        GRAPH_CALLS[name](plan, a, stream=stream)
+        assert streams == [stream]
+        assert made and all(s is stream for s, _ in made), made

@@ -3,6 +3,7 @@ current stream allocates and writes: nothing of a call may be given away before 
 
 import pytest
 
+import helpers
 from node_helpers import Problem
 
 pytestmark = pytest.mark.gpu
@@ -49,6 +50,26 @@ def test_node_operators(torch, irreps, n):
                              B.tpconv_dropout_backward(p.plan, gy, d, stream=st)),
                  lambda st: B.tpconv_dropout_norm_forward(p.plan, p.x, d, gy, p.w, p.b, stream=st),
                  lambda st: B.tpconv_dropout_norm_backward(p.plan, p.x, p.w, gy, d, t, stream=st)):
+        _check_on_a_busy_stream(torch, call, sizes)
+
+
+@pytest.mark.parametrize("cfg,n", [(1, 300), (3, 200)])
+def test_convolution_and_graph(torch, cfg, n):
+    """The same for the convolution's passes and the graph calls (uvw and uvu)."""
+    from equivariant_gnn_tensor_dst_b200 import binding as B
+    p = helpers.Problem(cfg, n_nodes=n)
+    lp = helpers.lib_plan(p.cfg)
+    x, pos, rp, src, W, g = (helpers.cuda(a) for a in (p.x, p.pos, p.row_ptr, p.src, p.W, p.gout))
+    views = B.tpconv_csr_transpose(rp, src, p.N)
+    perm = B.tpconv_spatial_order(pos)
+    sizes = [lp.workspace_bytes(p.N, p.E), W.numel() * 4, x.numel() * 4, g.numel() * 4, 4 * p.E, 4 * p.N + 4]
+    for call in (lambda st: (B.tpconv_forward(lp, x, pos, rp, src, W, stream=st),),
+                 lambda st: B.tpconv_backward(lp, x, pos, rp, src, *views, W, g, stream=st),
+                 lambda st: B.tpconv_double_backward(lp, x, pos, rp, src, *views, W, g, gg_x=x, gg_pos=pos, stream=st),
+                 lambda st: B.tpconv_csr_transpose(rp, src, p.N, stream=st),
+                 lambda st: (B.tpconv_validate_graph(rp, src, p.N, stream=st), B.tpconv_spatial_order(pos, stream=st),
+                             B.tpconv_gather_rows(x, perm, stream=st)),
+                 lambda st: B.tpconv_permute_graph(rp, src, perm, stream=st)):
         _check_on_a_busy_stream(torch, call, sizes)
 
 
