@@ -420,6 +420,8 @@ def tpconv_gather_rows(a, perm, stream=None):
     _need(a, torch.float32, "a")
     _need(perm, torch.int32, "perm")
     rows, width = a.shape[0], (a.numel() // a.shape[0] if a.shape[0] else 0)
+    if perm.numel() != rows:
+        raise ValueError(f"perm must have {rows} entries, not {perm.numel()}")
     with _on(stream):
         out = torch.empty_like(a)
     check(lib().tpconv_gather_rows(perm.numel(), width, _ptr(a), _ptr(perm), _ptr(out), _stream(stream)),

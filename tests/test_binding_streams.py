@@ -131,3 +131,12 @@ def test_convolution_and_graph_tensors_belong_to_the_stream(graph, made, name):
         GRAPH_CALLS[name](plan, a, stream=stream)
         assert streams == [stream]
         assert made and all(s is stream for s, _ in made), made
+
+
+@pytest.mark.parametrize("rows", [0, 7, 80])
+def test_gathered_rows_are_as_many_as_perm(graph, rows):
+    """The library reads and writes perm.numel() rows of arrays that have a.shape[0]."""
+    _, a, streams = graph
+    with pytest.raises(ValueError):
+        B.tpconv_gather_rows(a["x"], torch.ones(rows, dtype=torch.int32))
+    assert not streams
