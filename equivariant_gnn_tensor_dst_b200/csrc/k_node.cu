@@ -520,7 +520,8 @@ __device__ __forceinline__ void apply_mask(f2 (&v)[P], uint32_t keep, float scal
 
 // Whether the sum of squares about the mean, taken as a difference (sum of squares less mean times
 // sum), has to be taken again around the mean: the difference is exact to a few 2^-24 of itself while
-// the mean is at most twice the spread.  Also where it is no number.  All warps of a group have read the
+// the mean is at most twice the spread (and the sum of products with a to a few 2^-24 of |a|, which
+// the product in a has lost already).  Also where it is no number.  All warps of a group have read the
 // same values and added them in the same order, so all take the same way (and meet at its barrier).
 __device__ __forceinline__ bool large_mean(float mu, float S, float q) { return !(mu * mu * S <= 4.f * q); }
 
@@ -785,12 +786,16 @@ TPC_NODE_KERNEL(TH, PASS_BWD, 16 / sizeof(T) * J)
       shift_by<V, J, EDGE>(u, -mu, valid);
     }
     if (second) {
-      // mean(a) drops out of mean(a h) in a 0e block: h has no mean
-      f2 q0 = mul2(u[0], u[0]), q1 = mul2(u[0], product(0));
+      // mean(a) would drop out of mean(a h) in a 0e block if h had no mean, but u keeps the rounding of mu:
+      // with a less its mean, neither counts (means of 1000 in both, spreads of 1: grad_x to 3e-3, 0.2
+      // with mean(a) left in)
+      const f2 nma = both(-ma);
+      const auto rest = [&](int p) { return HOLD ? fma2(w[p], a[p], nma) : add2(a[p], nma); };
+      f2 q0 = mul2(u[0], u[0]), q1 = mul2(u[0], rest(0));
 #pragma unroll
       for (int p = 1; p < P; ++p) {
         q0 = fma2(u[p], u[p], q0);
-        q1 = fma2(u[p], product(p), q1);
+        q1 = fma2(u[p], rest(p), q1);
       }
       q[0] = lo(q0) + hi(q0);
       q[1] = lo(q1) + hi(q1);
