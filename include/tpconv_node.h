@@ -31,7 +31,8 @@
  * Shared conventions (as in tpconv.h)
  *  - Device pointers are 16-byte aligned (else TPCONV_ERR_MISALIGNED), rows contiguous, all
  *    node arrays of a call in the plan's type.  Arithmetic, statistics and sums are float32;
- *    each output is rounded once.  Sums of squares beyond float32's range give r = 0.
+ *    each output is rounded once.  Sums of squares about the mean beyond float32's range give r = 0,
+ *    a 0e block's sum beyond it NaN in that block of the row.
  *  - Every compute call is asynchronous on `stream`, allocates nothing, does not synchronise
  *    and may be captured into a CUDA graph.  Results are deterministic (no floating-point
  *    atomics; fixed order).  A row's results do not depend on the other rows; where rows do not

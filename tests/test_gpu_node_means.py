@@ -76,3 +76,32 @@ def test_fused_with_dropout_and_residual(irreps, n):
     assert np.all((gx.cpu().numpy() == 0) >= (mask == 0))
     # grad_x = mask * grad_residual: the scale's and the product's rounding
     _within(gx, mask * gr.double().cpu().numpy(), 3 * U * np.abs(mask * gr.double().cpu().numpy()), what="grad_x")
+
+
+@pytest.mark.parametrize("S", [96, 1001, 1024, 2048, 4096, 3999, 9001])
+@pytest.mark.parametrize("fused", [False, True])
+def test_sums_beyond_the_range_about_zero_but_not_about_the_mean(S, fused):
+    """Rows whose sum of squares passes float32's range while that about the mean does not, and in the
+    backward also the sum of products with the gradient: the same values whatever holds the row."""
+    from equivariant_gnn_tensor_dst_b200 import binding as B
+    n = 24
+    p = Problem(f"{S}x0e", n)
+    g = np.random.default_rng(3)
+    s = np.sqrt(1.2e38 / S)          # S s^2 = 1.2e38, S (s^2 + mean^2) = 5.5e38
+    p.x, p.x64 = stored(s * (np.clip(g.normal(size=(n, S)), -3, 3) + 1.9), "float32")
+    one, w64 = np.ones(S), np.ones(S)
+    for mean in (0.0, 20 * s):       # with the second, S mean(x) mean(grad) = 4.6e39
+        gy, gy64 = stored(mean + 0.05 * s * np.clip(g.normal(size=(n, S)), -3, 3), "float32")
+        if mean == 0.0:
+            gy, gy64 = stored(g.normal(size=(n, S)), "float32")
+        if fused:
+            got = B.tpconv_dropout_norm_backward(p.plan, p.x, None, gy, B.Dropout(0.0, 1))[1:]
+            y = B.tpconv_dropout_norm_forward(p.plan, p.x, B.Dropout(0.0, 1))[1]
+        else:
+            got = B.tpconv_norm_backward(p.plan, p.x, None, gy)
+            y = B.tpconv_norm_forward(p.plan, p.x)
+        zero = np.zeros(S)
+        _within(y, node.norm_forward(p.R, p.x64, one, zero), nm.forward_bound(p.R, p.x64, one, zero), what="y")
+        refs, bounds = node.norm_backward(p.R, p.x64, w64, gy64), nm.backward_bound(p.R, p.x64, w64, gy64)
+        for a, ref, bound, name in zip(got, refs, bounds, ("grad_x", "grad_weight", "grad_bias")):
+            _within(a, ref, bound, what=name)
