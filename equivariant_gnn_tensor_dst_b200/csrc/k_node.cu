@@ -174,12 +174,13 @@ struct Place {
   __device__ __forceinline__ int elem(int j) const { return (j * G + lane) * V - shift; }
 };
 
-// Slots of the copy ring.  A CTA keeps 12 KB of rows on the way in float32 (forward 50000 x 592: 41 us,
-// 47 us with 24 KB or more), 24 KB in 16 bits, where a row is half as long and takes as many
-// instructions (the same in bf16: 31 us with one row ahead, 26 us with 12 KB, 25 us with 24 KB).
+// Slots of the copy ring: the row that is computed, and as many rows on the way as make up 12 KB or more
+// for 256 threads in float32 (forward 50000 x 592: 41 us, 47 us with 24 KB or more), 24 KB in 16 bits,
+// where a row is half as long and takes as many instructions (the same in bf16: 31 us with one row ahead,
+// 26 us with 12 KB, 25 us with 24 KB).  One row on the way at least, which for three arrays of four packs
+// is 48 KB; CTAs of 512 threads have twice as much on the way.
 __host__ __device__ constexpr int ring_slots(int esize, int pack_bytes) {
-  const int rows = ((esize == 4 ? 12288 : 24576) + pack_bytes * kThreads - 1) / (pack_bytes * kThreads);
-  return rows > 7 ? 8 : rows + 1;
+  return ((esize == 4 ? 12288 : 24576) + pack_bytes * kThreads - 1) / (pack_bytes * kThreads) + 1;
 }
 
 // A thread's own packs of A arrays, copied ahead row by row.  Packs beyond the segment hold zeros
@@ -1296,9 +1297,15 @@ struct LaunchPlan {
   size_t floats = 0;   // partial sums
 };
 
-// Packs per lane that the kernels are built for: 1..most (run_packs).  At most 16 elements a lane, 12
-// (8 in 16 bits) in the double backward, whose five values per element fill the registers.
+// Most packs per lane: 16 elements, 12 (8 in 16 bits) in the double backward, whose five values per
+// element fill the registers.  CTAs of 512 threads have that many always.
 constexpr int most_packs(bool dbl, int esize) { return dbl ? (esize == 4 ? 3 : 1) : (esize == 4 ? 4 : 2); }
+// CTAs of 256 threads have 1 up to this: 8 elements in the passes with sums off the boundary, whose masks
+// take registers (backward 50000 x 145 f32: 28 us, 31 us with 12; f16: 26 us, 29 us with 16).
+constexpr int most_narrow_packs(Pass pass, bool edge, int esize) {
+  const int most = most_packs(pass == PASS_DBL, esize), eight = 8 * esize / 16;
+  return edge && pass != PASS_FWD && most > eight ? eight : most;
+}
 
 int log2_lanes(int elems, int per_lane) {
   int lg = 0;
@@ -1362,12 +1369,11 @@ LaunchPlan plan_launches(const Shape& sh, const NodeDesc& D, long long N) {
       // Fewest lane-packs per row (a segment's lanes are a power of two); of equal ones the most
       // packs per lane, but 12 elements in the passes with sums and in dropout alone (fused backward
       // 50000 x 592 f32: 104 us, 112 us with 16), 8 in the double backward (the same rows: 105 us, 110
-      // us with 12) and in the passes with sums off the boundary, whose masks take registers (backward
-      // 50000 x 145 f32: 28 us, 31 us with 12; f16: 26 us, 29 us with 16).
-      const int lg_max = log2_lanes(L.threads, 1), few = (P.edge && sums) || sh.pass == PASS_DBL ? 8 : !P.edge && (sums || !sh.norm) ? 12 : 16;
+      // us with 12).
+      const int lg_max = log2_lanes(L.threads, 1), few = sh.pass == PASS_DBL ? 8 : !P.edge && (sums || !sh.norm) ? 12 : 16;
+      const int most = kd == KIND_WIDE ? jmax : most_narrow_packs(sh.pass, P.edge, sh.esize);
       long long best = -1;
-      for (int j = kd == KIND_WIDE ? jmax : 1; j <= jmax; ++j) {
-        if (P.edge && sums && V * j > few && best >= 0) break;
+      for (int j = kd == KIND_WIDE ? jmax : 1; j <= most; ++j) {
         long long cost = 0;
         bool fits = true;
         for (int k = 0; k < M.n; ++k) {
@@ -1471,36 +1477,43 @@ void launch(void (*kernel)(Ps...), std::atomic<uint64_t>& allowed, const Call& c
   launch_early(kernel, L.ctas, L.threads, L.smem, c.s, args...);
 }
 
-template <class T, int J, int TH, bool EDGE>
+// Only kernels that some rows reach are built: dropout alone in 16 bits has rows off the boundary here
+// (k_drop has the others).
+template <class T, int J, int TH, bool EDGE, Pass PASS>
 void run_kernel(const Call& c, const Launch& L) {
-  constexpr bool dbl = J <= most_packs(true, sizeof(T));
-  static std::atomic<uint64_t> ok[6];  // devices, by kernel
-  if (c.pass == PASS_FWD) {
-    if (c.drop && c.norm) launch(k_fwd<T, J, TH, EDGE, true, true>, ok[0], c, L, c.D, L.M, c.d, c.A, c.N);
-    else if (c.drop) launch(k_fwd<T, J, TH, EDGE, true, false>, ok[1], c, L, c.D, L.M, c.d, c.A, c.N);
-    else launch(k_fwd<T, J, TH, EDGE, false, true>, ok[2], c, L, c.D, L.M, c.d, c.A, c.N);
-  } else if (c.pass == PASS_BWD) {
-    if (c.drop) launch(k_bwd<T, J, TH, EDGE, true>, ok[3], c, L, c.D, L.M, c.d, c.A, c.N);
-    else launch(k_bwd<T, J, TH, EDGE, false>, ok[4], c, L, c.D, L.M, c.d, c.A, c.N);
-  } else if constexpr (dbl) {
-    launch(k_dbl<T, J, TH, EDGE>, ok[5], c, L, c.D, L.M, c.A, c.N);
+  static std::atomic<uint64_t> ok[3];  // devices, by kernel
+  if constexpr (PASS == PASS_FWD) {
+    if (!c.drop) {
+      launch(k_fwd<T, J, TH, EDGE, false, true>, ok[0], c, L, c.D, L.M, c.d, c.A, c.N);
+    } else if (c.norm) {
+      launch(k_fwd<T, J, TH, EDGE, true, true>, ok[1], c, L, c.D, L.M, c.d, c.A, c.N);
+    } else if constexpr (sizeof(T) == 4 || EDGE) {
+      launch(k_fwd<T, J, TH, EDGE, true, false>, ok[2], c, L, c.D, L.M, c.d, c.A, c.N);
+    }
+  } else if constexpr (PASS == PASS_BWD) {
+    if (c.drop) launch(k_bwd<T, J, TH, EDGE, true>, ok[0], c, L, c.D, L.M, c.d, c.A, c.N);
+    else launch(k_bwd<T, J, TH, EDGE, false>, ok[1], c, L, c.D, L.M, c.d, c.A, c.N);
+  } else {
+    launch(k_dbl<T, J, TH, EDGE>, ok[0], c, L, c.D, L.M, c.A, c.N);
+  }
+}
+
+template <class T, bool EDGE, Pass PASS, int J = 1>
+void run_packs(const Call& c, const Launch& L) {
+  if (L.kind == KIND_WIDE) {
+    if constexpr (J == 1) run_kernel<T, most_packs(PASS == PASS_DBL, sizeof(T)), kWide, EDGE, PASS>(c, L);
+  } else if (L.J == J) {
+    run_kernel<T, J, kThreads, EDGE, PASS>(c, L);
+  } else if constexpr (J < most_narrow_packs(PASS, EDGE, sizeof(T))) {
+    run_packs<T, EDGE, PASS, J + 1>(c, L);
   }
 }
 
 template <class T, bool EDGE>
-void run_packs(const Call& c, const Launch& L) {
-  constexpr int most = most_packs(false, sizeof(T)), dbl = most_packs(true, sizeof(T));
-  if (L.kind == KIND_WIDE) {
-    if (L.J == most) run_kernel<T, most, kWide, EDGE>(c, L);
-    else run_kernel<T, dbl, kWide, EDGE>(c, L);
-    return;
-  }
-  if (L.J == 1) run_kernel<T, 1, kThreads, EDGE>(c, L);
-  if (L.J == 2) run_kernel<T, 2, kThreads, EDGE>(c, L);
-  if constexpr (most == 4) {
-    if (L.J == 3) run_kernel<T, 3, kThreads, EDGE>(c, L);
-    if (L.J == 4) run_kernel<T, 4, kThreads, EDGE>(c, L);
-  }
+void run_pass(const Call& c, const Launch& L) {
+  if (c.pass == PASS_FWD) run_packs<T, EDGE, PASS_FWD>(c, L);
+  else if (c.pass == PASS_BWD) run_packs<T, EDGE, PASS_BWD>(c, L);
+  else run_packs<T, EDGE, PASS_DBL>(c, L);
 }
 
 template <class T>
@@ -1558,8 +1571,8 @@ cudaError_t run_node(const Call& c) {
   for (int i = 0; i < P.n; ++i) {
     const Launch& L = P.l[i];
     if (L.kind == KIND_ANY) run_any<T>(c, L);
-    else if (P.edge) run_packs<T, true>(c, L);
-    else run_packs<T, false>(c, L);
+    else if (P.edge) run_pass<T, true>(c, L);
+    else run_pass<T, false>(c, L);
   }
   if (c.A.partial && P.parts.n)
     launch_early(k_norm_reduce, (c.D.channels + c.D.biases + 31) / 32, 32 * kShares, 0, c.s, c.D, P.parts,
