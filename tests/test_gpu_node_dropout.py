@@ -86,6 +86,26 @@ def test_in_place(torch):
         assert torch.equal(B.tpconv_dropout_forward(q.plan, q.x, _drop(0.3), residual=b, out=b), ref)
 
 
+@pytest.mark.parametrize("irreps,dtype", [(i, d) for i in (MIXED, ODD, "64x0e+24x1o", "3000x0e", "4100x1o", "20001x0e")
+                                          for d in TYPES])
+@pytest.mark.parametrize("layout", ["ir_mul", "mul_ir"])
+def test_in_place_in_every_kernel(torch, irreps, dtype, layout):
+    """out equal to x, to the residual and to both, in each storage type: whole packs, rows off the
+    boundary, segments wider than a CTA's registers."""
+    from equivariant_gnn_tensor_dst_b200 import binding as B
+    q = Problem(irreps, 37, dtype, layout)
+    res, _ = q.rows()
+    plain = B.tpconv_dropout_forward(q.plan, q.x, _drop(0.3))
+    ref = B.tpconv_dropout_forward(q.plan, q.x, _drop(0.3), residual=res)
+    own = B.tpconv_dropout_forward(q.plan, q.x, _drop(0.3), residual=q.x)
+    a, b, c, d, e = q.x.clone(), res.clone(), q.x.clone(), q.x.clone(), q.x.clone()
+    assert torch.equal(B.tpconv_dropout_forward(q.plan, a, _drop(0.3), residual=res, out=a), ref)
+    assert torch.equal(B.tpconv_dropout_forward(q.plan, q.x, _drop(0.3), residual=b, out=b), ref)
+    assert torch.equal(B.tpconv_dropout_forward(q.plan, c, _drop(0.3), residual=c, out=c), own)
+    assert torch.equal(B.tpconv_dropout_forward(q.plan, d, _drop(0.3), out=d), plain)
+    assert torch.equal(B.tpconv_dropout_backward(q.plan, e, _drop(0.3), out=e), plain)
+
+
 def test_step_counter_and_replay(torch):
     """A captured graph draws the mask of offset + *step as it is when the graph runs."""
     from equivariant_gnn_tensor_dst_b200 import binding as B
