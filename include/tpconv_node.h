@@ -4,12 +4,15 @@
  * Rows are the node rows of tpconv.h: irrep blocks in the order of the irreps string, a
  * block of C channels and order l holding S = (2l+1) C elements, stored [2l+1][C]
  * (TPCONV_LAYOUT_IR_MUL) or [C][2l+1] (TPCONV_LAYOUT_MUL_IR).  The operators also serve
- * rows that are not node features, e.g. "64x0e" for a scalar edge embedding.
+ * rows that are not node features, e.g. "64x0e" for a scalar edge embedding.  The
+ * convolution of tpconv.h takes float32 rows alone: 16-bit rows are cast on either side.
  *
  * Layer norm (Ba, Kiros, Hinton, arXiv 1607.06450), block by block.  For the S elements
  * v of one block of one row, with channel c(s) of element s:
- *     u = v - mean(v)  for 0e blocks,   u = v  otherwise (a mean of l > 0 or odd
- *                                        elements would not commute with O(3))
+ *     u = v - mean(v)  for 0e blocks,   u = v  otherwise (a mean over the elements of an
+ *                                        l > 0 block mixes components, and does not commute
+ *                                        with rotations; 0o blocks, which have no bias, are
+ *                                        not centred either)
  *     q = mean(u^2),  r = 1 / sqrt(q + eps),  h = r u
  *     y_s = weight_c h_s + bias_c       (bias for 0e blocks alone)
  * so y is equivariant: r is invariant, and weight and bias act per channel.
