@@ -6,7 +6,6 @@ allocate outputs and workspaces and to name the current CUDA stream.  If the sha
 library is missing the import of ``lib()`` fails loudly; there is no fallback.
 """
 
-import contextlib
 import ctypes
 import os
 
@@ -198,20 +197,35 @@ class Plan:
 # ---------------------------------------------------------------------------
 # torch-facing calls
 #
-# A call with stream= makes its outputs and its workspace on that stream, as calls inside
-# torch.cuda.stream(stream) do: inputs have to be ready there, and outputs that are used on another
-# stream follow torch's rule for such tensors (wait for the stream; Tensor.record_stream before the
-# tensor is dropped).
+# A call with stream= runs as inside torch.cuda.stream(stream): inputs have to be ready there, and
+# outputs that are used on another stream follow torch's rule for such tensors (wait for the stream;
+# Tensor.record_stream before the tensor is dropped).
 # ---------------------------------------------------------------------------
 
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream):
+def _stream():
     import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+def _on(call, args):
+    """A call with its arguments (by name, its stream among them) on that stream: its outputs and its
+    workspace are made there, too.  The allocator gives a block away again in the order of the stream
+    that it was made on, so a workspace that is dropped when the call returns, its kernels still queued,
+    is safe there, and a new block has no work of another stream pending."""
+    import torch
+    stream = args.pop("stream")
+    if (stream.cuda_stream == torch._C._cuda_getCurrentRawStream(stream.device_index)
+            and stream.device_index == torch._C._cuda_getDevice()):
+        return call(**args)     # entering the current stream all the same takes ten microseconds
+    for name, a in args.items():
+        if isinstance(a, torch.Tensor) and a.get_device() != stream.device_index:
+            raise ValueError(f"the stream is on {stream.device}, {name} on {a.device}")
+    with torch.cuda.stream(stream):
+        return call(**args)
 
 
 def _need(t, dtype, name):
@@ -226,106 +240,97 @@ def _need(t, dtype, name):
         raise ValueError(f"{name} must be contiguous")
 
 
-_CURRENT = contextlib.nullcontext()
-
-
-def _on(stream):
-    """Where a call makes its own tensors: on the stream that its kernels run on (None: the current one).
-    The allocator gives a block away again in the order of its stream, so a workspace that is dropped
-    when the call returns, its kernels still queued, is safe there, and a new block has no work of
-    another stream pending."""
-    if stream is None:
-        return _CURRENT
-    import torch
-    return torch.cuda.stream(stream)
-
-
 def workspace(nbytes, device):
     import torch
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
 def tpconv_csr_transpose(row_ptr, src, n_nodes, stream=None):
+    if stream is not None:
+        return _on(tpconv_csr_transpose, locals())
     import torch
     _need(row_ptr, torch.int32, "row_ptr")
     _need(src, torch.int32, "src")
     E = src.numel()
     dev = row_ptr.device
+    t_ptr = torch.empty(n_nodes + 1, dtype=torch.int32, device=dev)
+    t_eid = torch.empty(max(E, 1), dtype=torch.int32, device=dev)
+    t_dst = torch.empty(max(E, 1), dtype=torch.int32, device=dev)
     nb = ctypes.c_size_t()
     check(lib().tpconv_csr_transpose_workspace_bytes(n_nodes, E, ctypes.byref(nb)))
-    with _on(stream):
-        t_ptr = torch.empty(n_nodes + 1, dtype=torch.int32, device=dev)
-        t_eid = torch.empty(max(E, 1), dtype=torch.int32, device=dev)
-        t_dst = torch.empty(max(E, 1), dtype=torch.int32, device=dev)
-        ws = workspace(nb.value, dev)
+    ws = workspace(nb.value, dev)
     check(lib().tpconv_csr_transpose(n_nodes, E, _ptr(row_ptr), _ptr(src), _ptr(t_ptr), _ptr(t_eid),
-                                     _ptr(t_dst), _ptr(ws), ws.numel(), _stream(stream)),
+                                     _ptr(t_dst), _ptr(ws), ws.numel(), _stream()),
           "tpconv_csr_transpose")
     return t_ptr, t_eid[:E], t_dst[:E]
 
 
 def tpconv_validate_graph(row_ptr, src, n_nodes, stream=None):
+    if stream is not None:
+        return _on(tpconv_validate_graph, locals())
     import torch
-    with _on(stream):
-        err = torch.zeros(4, dtype=torch.int32, device=row_ptr.device)
+    err = torch.zeros(4, dtype=torch.int32, device=row_ptr.device)
     check(lib().tpconv_validate_graph(n_nodes, src.numel(), _ptr(row_ptr), _ptr(src), _ptr(err),
-                                      _stream(stream)), "tpconv_validate_graph")
+                                      _stream()), "tpconv_validate_graph")
     return err[:1]
 
 
 def tpconv_forward(plan, x, pos, row_ptr, src, W, out=None, ws=None, stream=None):
+    if stream is not None:
+        return _on(tpconv_forward, locals())
     import torch
     for t, n in ((x, "x"), (pos, "pos"), (W, "W")):
         _need(t, torch.float32, n)
     _need(row_ptr, torch.int32, "row_ptr")
     _need(src, torch.int32, "src")
     N, E = pos.shape[0], src.numel()
-    with _on(stream):
-        if out is None:
-            out = torch.empty(N, plan.dim_out, dtype=torch.float32, device=x.device)
-        if ws is None:
-            ws = workspace(plan.workspace_bytes(N, E, PASS_FORWARD), x.device)
+    if out is None:
+        out = torch.empty(N, plan.dim_out, dtype=torch.float32, device=x.device)
+    if ws is None:
+        ws = workspace(plan.workspace_bytes(N, E, PASS_FORWARD), x.device)
     check(lib().tpconv_forward(plan.handle, N, E, _ptr(x), _ptr(pos), _ptr(row_ptr), _ptr(src), _ptr(W),
-                               _ptr(out), _ptr(ws), ws.numel(), _stream(stream)), "tpconv_forward")
+                               _ptr(out), _ptr(ws), ws.numel(), _stream()), "tpconv_forward")
     return out
 
 
 def tpconv_backward(plan, x, pos, row_ptr, src, t_ptr, t_eid, t_dst, W, grad_out, need_x=True,
                     need_pos=True, need_W=True, ws=None, outputs=None, stream=None):
+    if stream is not None:
+        return _on(tpconv_backward, locals())
     import torch
     N, E = pos.shape[0], src.numel()
     dev = x.device
-    with _on(stream):
-        if outputs is None:
-            gx = torch.empty(N, plan.dim_in, dtype=torch.float32, device=dev) if need_x else None
-            gp = torch.empty(N, 3, dtype=torch.float32, device=dev) if need_pos else None
-            gw = torch.empty(plan.num_basis, plan.weight_cols, dtype=torch.float32, device=dev) if need_W else None
-        else:
-            gx, gp, gw = outputs
-        if ws is None:
-            ws = workspace(plan.workspace_bytes(N, E, PASS_BACKWARD), dev)
+    if outputs is None:
+        gx = torch.empty(N, plan.dim_in, dtype=torch.float32, device=dev) if need_x else None
+        gp = torch.empty(N, 3, dtype=torch.float32, device=dev) if need_pos else None
+        gw = torch.empty(plan.num_basis, plan.weight_cols, dtype=torch.float32, device=dev) if need_W else None
+    else:
+        gx, gp, gw = outputs
+    if ws is None:
+        ws = workspace(plan.workspace_bytes(N, E, PASS_BACKWARD), dev)
     check(lib().tpconv_backward(plan.handle, N, E, _ptr(x), _ptr(pos), _ptr(row_ptr), _ptr(src),
                                 _ptr(t_ptr), _ptr(t_eid), _ptr(t_dst), _ptr(W), _ptr(grad_out),
-                                _ptr(gx), _ptr(gp), _ptr(gw), _ptr(ws), ws.numel(), _stream(stream)),
+                                _ptr(gx), _ptr(gp), _ptr(gw), _ptr(ws), ws.numel(), _stream()),
           "tpconv_backward")
     return gx, gp, gw
 
 
 def tpconv_forward_embedded(plan, x, Y, phi, row_ptr, src, W, out=None, ws=None, stream=None):
     """Forward with the edge embedding given per edge: Y [E, (lmax+1)^2], phi [E, K]."""
+    if stream is not None:
+        return _on(tpconv_forward_embedded, locals())
     import torch
     for t, n in ((x, "x"), (Y, "Y"), (phi, "phi"), (W, "W")):
         _need(t, torch.float32, n)
     _need(row_ptr, torch.int32, "row_ptr")
     _need(src, torch.int32, "src")
     N, E = row_ptr.numel() - 1, src.numel()
-    with _on(stream):
-        if out is None:
-            out = torch.empty(N, plan.dim_out, dtype=torch.float32, device=x.device)
-        if ws is None:
-            ws = workspace(plan.workspace_bytes(N, E, PASS_FORWARD), x.device)
+    if out is None:
+        out = torch.empty(N, plan.dim_out, dtype=torch.float32, device=x.device)
+    if ws is None:
+        ws = workspace(plan.workspace_bytes(N, E, PASS_FORWARD), x.device)
     check(lib().tpconv_forward_embedded(plan.handle, N, E, _ptr(x), _ptr(Y), _ptr(phi), _ptr(row_ptr), _ptr(src),
-                                        _ptr(W), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)),
+                                        _ptr(W), _ptr(out), _ptr(ws), ws.numel(), _stream()),
           "tpconv_forward_embedded")
     return out
 
@@ -333,23 +338,24 @@ def tpconv_forward_embedded(plan, x, Y, phi, row_ptr, src, W, out=None, ws=None,
 def tpconv_backward_embedded(plan, x, Y, phi, row_ptr, src, t_ptr, t_eid, t_dst, W, grad_out, need_x=True,
                              need_W=True, need_phi=True, need_Y=True, ws=None, outputs=None, stream=None):
     """Returns (grad_x, grad_W, grad_phi [E, K], grad_Y [E, (lmax+1)^2])."""
+    if stream is not None:
+        return _on(tpconv_backward_embedded, locals())
     import torch
     N, E = row_ptr.numel() - 1, src.numel()
     dev = x.device
-    with _on(stream):
-        if outputs is None:
-            gx = torch.empty(N, plan.dim_in, dtype=torch.float32, device=dev) if need_x else None
-            gw = torch.empty(plan.num_basis, plan.weight_cols, dtype=torch.float32, device=dev) if need_W else None
-            gphi = torch.empty(E, plan.num_basis, dtype=torch.float32, device=dev) if need_phi else None
-            gY = torch.empty(E, Y.shape[1], dtype=torch.float32, device=dev) if need_Y else None
-        else:
-            gx, gw, gphi, gY = outputs
-        if ws is None:
-            ws = workspace(plan.workspace_bytes(N, E, PASS_BACKWARD), dev)
+    if outputs is None:
+        gx = torch.empty(N, plan.dim_in, dtype=torch.float32, device=dev) if need_x else None
+        gw = torch.empty(plan.num_basis, plan.weight_cols, dtype=torch.float32, device=dev) if need_W else None
+        gphi = torch.empty(E, plan.num_basis, dtype=torch.float32, device=dev) if need_phi else None
+        gY = torch.empty(E, Y.shape[1], dtype=torch.float32, device=dev) if need_Y else None
+    else:
+        gx, gw, gphi, gY = outputs
+    if ws is None:
+        ws = workspace(plan.workspace_bytes(N, E, PASS_BACKWARD), dev)
     check(lib().tpconv_backward_embedded(plan.handle, N, E, _ptr(x), _ptr(Y), _ptr(phi), _ptr(row_ptr), _ptr(src),
                                          _ptr(t_ptr), _ptr(t_eid), _ptr(t_dst), _ptr(W), _ptr(grad_out),
                                          _ptr(gx), _ptr(gw), _ptr(gphi), _ptr(gY), _ptr(ws), ws.numel(),
-                                         _stream(stream)),
+                                         _stream()),
           "tpconv_backward_embedded")
     return gx, gw, gphi, gY
 
@@ -359,72 +365,76 @@ def tpconv_double_backward(plan, x, pos, row_ptr, src, t_ptr, t_eid, t_dst, W, g
                            need_pos=False, ws=None, outputs=None, stream=None):
     """Returns (grad_x, grad_W, grad_grad_out), plus grad_pos [N, 3] when need_pos
     (``outputs`` then has four entries)."""
+    if stream is not None:
+        return _on(tpconv_double_backward, locals())
     import torch
     N, E = pos.shape[0], src.numel()
     dev = x.device
-    with _on(stream):
-        if outputs is None:
-            gx = torch.empty(N, plan.dim_in, dtype=torch.float32, device=dev) if need_x else None
-            gw = torch.empty(plan.num_basis, plan.weight_cols, dtype=torch.float32, device=dev) if need_W else None
-            gg = torch.empty(N, plan.dim_out, dtype=torch.float32, device=dev) if need_grad_out else None
-            gp = torch.empty(N, 3, dtype=torch.float32, device=dev) if need_pos else None
-        elif need_pos:
-            gx, gw, gg, gp = outputs
-        else:
-            (gx, gw, gg), gp = outputs, None
-        if ws is None:
-            ws = workspace(plan.workspace_bytes(N, E, PASS_DOUBLE_BACKWARD), dev)
+    if outputs is None:
+        gx = torch.empty(N, plan.dim_in, dtype=torch.float32, device=dev) if need_x else None
+        gw = torch.empty(plan.num_basis, plan.weight_cols, dtype=torch.float32, device=dev) if need_W else None
+        gg = torch.empty(N, plan.dim_out, dtype=torch.float32, device=dev) if need_grad_out else None
+        gp = torch.empty(N, 3, dtype=torch.float32, device=dev) if need_pos else None
+    elif need_pos:
+        gx, gw, gg, gp = outputs
+    else:
+        (gx, gw, gg), gp = outputs, None
+    if ws is None:
+        ws = workspace(plan.workspace_bytes(N, E, PASS_DOUBLE_BACKWARD), dev)
     check(lib().tpconv_double_backward(plan.handle, N, E, _ptr(x), _ptr(pos), _ptr(row_ptr), _ptr(src),
                                        _ptr(t_ptr), _ptr(t_eid), _ptr(t_dst), _ptr(W), _ptr(grad_out),
                                        _ptr(gg_x), _ptr(gg_pos), _ptr(gg_W), _ptr(gx), _ptr(gw), _ptr(gg),
-                                       _ptr(gp), _ptr(ws), ws.numel(), _stream(stream)),
+                                       _ptr(gp), _ptr(ws), ws.numel(), _stream()),
           "tpconv_double_backward")
     return (gx, gw, gg, gp) if need_pos else (gx, gw, gg)
 
 
 def tpconv_spatial_order(pos, stream=None):
     """perm [N] int32: nodes in Morton order of their positions (perm[k] = old id)."""
+    if stream is not None:
+        return _on(tpconv_spatial_order, locals())
     import torch
     _need(pos, torch.float32, "pos")
     N = pos.shape[0]
+    perm = torch.empty(max(N, 1), dtype=torch.int32, device=pos.device)
     nb = ctypes.c_size_t()
     check(lib().tpconv_spatial_order_workspace_bytes(N, ctypes.byref(nb)), "tpconv_spatial_order_workspace_bytes")
-    with _on(stream):
-        perm = torch.empty(max(N, 1), dtype=torch.int32, device=pos.device)
-        ws = workspace(nb.value, pos.device)
-    check(lib().tpconv_spatial_order(N, _ptr(pos), _ptr(perm), _ptr(ws), ws.numel(), _stream(stream)),
+    ws = workspace(nb.value, pos.device)
+    check(lib().tpconv_spatial_order(N, _ptr(pos), _ptr(perm), _ptr(ws), ws.numel(), _stream()),
           "tpconv_spatial_order")
     return perm[:N]
 
 
 def tpconv_permute_graph(row_ptr, src, perm, stream=None):
     """The receiver CSR renumbered by perm: (row_ptr_out, src_out, inv)."""
+    if stream is not None:
+        return _on(tpconv_permute_graph, locals())
     import torch
     _need(row_ptr, torch.int32, "row_ptr")
     _need(src, torch.int32, "src")
     _need(perm, torch.int32, "perm")
     N, E = row_ptr.numel() - 1, src.numel()
     dev = row_ptr.device
-    with _on(stream):
-        rp = torch.empty(N + 1, dtype=torch.int32, device=dev)
-        so = torch.empty(max(E, 1), dtype=torch.int32, device=dev)
-        inv = torch.empty(max(N, 1), dtype=torch.int32, device=dev)
+    rp = torch.empty(N + 1, dtype=torch.int32, device=dev)
+    so = torch.empty(max(E, 1), dtype=torch.int32, device=dev)
+    inv = torch.empty(max(N, 1), dtype=torch.int32, device=dev)
     check(lib().tpconv_permute_graph(N, E, _ptr(row_ptr), _ptr(src), _ptr(perm), _ptr(rp), _ptr(so), _ptr(inv),
-                                     _stream(stream)), "tpconv_permute_graph")
+                                     _stream()), "tpconv_permute_graph")
     return rp, so[:E], inv[:N]
 
 
 def tpconv_gather_rows(a, perm, stream=None):
     """out[k] = a[perm[k]] for a 2-D float32 array (node features, positions)."""
+    if stream is not None:
+        return _on(tpconv_gather_rows, locals())
     import torch
     _need(a, torch.float32, "a")
     _need(perm, torch.int32, "perm")
     rows, width = a.shape[0], (a.numel() // a.shape[0] if a.shape[0] else 0)
     if perm.numel() != rows:
         raise ValueError(f"perm must have {rows} entries, not {perm.numel()}")
-    with _on(stream):
-        out = torch.empty_like(a)
-    check(lib().tpconv_gather_rows(perm.numel(), width, _ptr(a), _ptr(perm), _ptr(out), _stream(stream)),
+    out = torch.empty_like(a)
+    check(lib().tpconv_gather_rows(perm.numel(), width, _ptr(a), _ptr(perm), _ptr(out), _stream()),
           "tpconv_gather_rows")
     return out
 
@@ -581,21 +591,20 @@ def _node_sums(like, n, need, device):
     return t, t.data_ptr()
 
 
-def _node_call(device, name, stream, *args):
-    """One library call on the tensors' device and the given (or that device's current) stream."""
+def _node_call(device, name, *args):
+    """One library call on the tensors' device and that device's current stream."""
     if device.index != _torch._C._cuda_getDevice():
         with _torch.cuda.device(device):
-            return _node_call(device, name, stream, *args)
+            return _node_call(device, name, *args)
     # the handle itself: building a torch Stream object costs several microseconds
-    raw = _torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    raw = _torch._C._cuda_getCurrentRawStream(device.index)
     status = getattr(_lib, name)(*args, raw)
     if status:
         raise TPConvError(status, name)
 
 
 def _node_ws(plan, N, ws, device):
-    """(workspace, address, bytes); a new one belongs to the stream that it is made on, and its owner may drop it
-    once the kernels that use it are queued there"""
+    """(workspace, address, bytes)"""
     if ws is None:
         ws = workspace(plan.workspace_bytes(N), device)
     elif ws.device != device or not ws.is_contiguous():
@@ -605,85 +614,91 @@ def _node_ws(plan, N, ws, device):
 
 def tpconv_norm_forward(plan, x, weight=None, bias=None, out=None, stream=None):
     """Irreps layer norm of node rows x [N, dim]; weight [channels], bias [biases] float32."""
+    if stream is not None:
+        return _on(tpconv_norm_forward, locals())
     px = _node_x(plan, x, "x")
     pw, pb = _node_vec(weight, plan.channels, "weight", x), _node_vec(bias, plan.biases, "bias", x)
-    with _on(stream):
-        out, po = _node_new(x, True) if out is None else (out, _node_row(out, "out", x))
-    _node_call(x.device, "tpconv_norm_forward", stream, plan._h, x.shape[0], px, pw, pb, po)
+    out, po = _node_new(x, True) if out is None else (out, _node_row(out, "out", x))
+    _node_call(x.device, "tpconv_norm_forward", plan._h, x.shape[0], px, pw, pb, po)
     return out
 
 
 def tpconv_norm_backward(plan, x, weight, grad_y, need_x=True, need_weight=True, need_bias=True, ws=None,
                          outputs=None, stream=None):
     """Returns (grad_x [N, dim], grad_weight [channels], grad_bias [biases])."""
+    if stream is not None:
+        return _on(tpconv_norm_backward, locals())
     dev, N, C, Cb = x.device, x.shape[0], plan.channels, plan.biases
     px, pg, pw = _node_x(plan, x, "x"), _node_row(grad_y, "grad_y", x), _node_vec(weight, C, "weight", x)
-    with _on(stream):
-        if outputs is None:
-            gx, pgx = _node_new(x, need_x)
-            gw, pgw = _node_sums(weight, C, need_weight, dev)
-            gb, pgb = _node_sums(None, Cb, need_bias, dev)
-        else:
-            gx, gw, gb = outputs
-            pgx = _node_row(gx, "grad_x", x)
-            pgw, pgb = _node_vec(gw, C, "grad_weight", x), _node_vec(gb, Cb, "grad_bias", x)
-        ws, pws, nws = _node_ws(plan, N, ws, dev)
-    _node_call(dev, "tpconv_norm_backward", stream, plan._h, N, px, pw, pg, pgx, pgw, pgb, pws, nws)
+    if outputs is None:
+        gx, pgx = _node_new(x, need_x)
+        gw, pgw = _node_sums(weight, C, need_weight, dev)
+        gb, pgb = _node_sums(None, Cb, need_bias, dev)
+    else:
+        gx, gw, gb = outputs
+        pgx = _node_row(gx, "grad_x", x)
+        pgw, pgb = _node_vec(gw, C, "grad_weight", x), _node_vec(gb, Cb, "grad_bias", x)
+    ws, pws, nws = _node_ws(plan, N, ws, dev)
+    _node_call(dev, "tpconv_norm_backward", plan._h, N, px, pw, pg, pgx, pgw, pgb, pws, nws)
     return gx, gw, gb
 
 
 def tpconv_norm_double_backward(plan, x, weight, grad_y, gg_x=None, gg_weight=None, gg_bias=None, need_x=True,
                                 need_weight=True, need_grad_y=True, ws=None, outputs=None, stream=None):
     """Returns (grad_x [N, dim], grad_weight [channels], grad_grad_y [N, dim])."""
+    if stream is not None:
+        return _on(tpconv_norm_double_backward, locals())
     dev, N, C = x.device, x.shape[0], plan.channels
     px, pg, pp = _node_x(plan, x, "x"), _node_row(grad_y, "grad_y", x), _node_row(gg_x, "gg_x", x)
     pw, pt = _node_vec(weight, C, "weight", x), _node_vec(gg_weight, C, "gg_weight", x)
     ptb = _node_vec(gg_bias, plan.biases, "gg_bias", x)
-    with _on(stream):
-        if outputs is None:
-            gx, pgx = _node_new(x, need_x)
-            gw, pgw = _node_sums(weight, C, need_weight, dev)
-            gg, pgg = _node_new(x, need_grad_y)
-        else:
-            gx, gw, gg = outputs
-            pgx, pgg = _node_row(gx, "grad_x", x), _node_row(gg, "grad_grad_y", x)
-            pgw = _node_vec(gw, C, "grad_weight", x)
-        ws, pws, nws = _node_ws(plan, N, ws, dev)
-    _node_call(dev, "tpconv_norm_double_backward", stream, plan._h, N, px, pw, pg, pp, pt, ptb, pgx, pgw, pgg, pws,
+    if outputs is None:
+        gx, pgx = _node_new(x, need_x)
+        gw, pgw = _node_sums(weight, C, need_weight, dev)
+        gg, pgg = _node_new(x, need_grad_y)
+    else:
+        gx, gw, gg = outputs
+        pgx, pgg = _node_row(gx, "grad_x", x), _node_row(gg, "grad_grad_y", x)
+        pgw = _node_vec(gw, C, "grad_weight", x)
+    ws, pws, nws = _node_ws(plan, N, ws, dev)
+    _node_call(dev, "tpconv_norm_double_backward", plan._h, N, px, pw, pg, pp, pt, ptb, pgx, pgw, pgg, pws,
                nws)
     return gx, gw, gg
 
 
 def tpconv_dropout_forward(plan, x, dropout, residual=None, out=None, stream=None):
     """residual + dropout(x); ``dropout`` is a Dropout.  out may be x or residual (in place)."""
+    if stream is not None:
+        return _on(tpconv_dropout_forward, locals())
     px, pr = _node_x(plan, x, "x"), _node_row(residual, "residual", x)
-    with _on(stream):
-        out, po = _node_new(x, True) if out is None else (out, _node_row(out, "out", x))
-    _node_call(x.device, "tpconv_dropout_forward", stream, plan._h, x.shape[0], px, pr, dropout.spec(x.device), po)
+    out, po = _node_new(x, True) if out is None else (out, _node_row(out, "out", x))
+    _node_call(x.device, "tpconv_dropout_forward", plan._h, x.shape[0], px, pr, dropout.spec(x.device), po)
     return out
 
 
 def tpconv_dropout_backward(plan, grad_out, dropout, out=None, stream=None):
     """grad_x of tpconv_dropout_forward (the residual's gradient is grad_out itself)."""
+    if stream is not None:
+        return _on(tpconv_dropout_backward, locals())
     pg = _node_x(plan, grad_out, "grad_out")
-    with _on(stream):
-        out, po = _node_new(grad_out, True) if out is None else (out, _node_row(out, "out", grad_out))
-    _node_call(grad_out.device, "tpconv_dropout_backward", stream, plan._h, grad_out.shape[0], pg,
+    out, po = _node_new(grad_out, True) if out is None else (out, _node_row(out, "out", grad_out))
+    _node_call(grad_out.device, "tpconv_dropout_backward", plan._h, grad_out.shape[0], pg,
                dropout.spec(grad_out.device), po)
     return out
 
 
 def tpconv_dropout_norm_forward(plan, x, dropout, residual=None, weight=None, bias=None, outputs=None, stream=None):
     """Returns (z, y): z = residual + dropout(x), y = norm(z)."""
+    if stream is not None:
+        return _on(tpconv_dropout_norm_forward, locals())
     px, pr = _node_x(plan, x, "x"), _node_row(residual, "residual", x)
     pw, pb = _node_vec(weight, plan.channels, "weight", x), _node_vec(bias, plan.biases, "bias", x)
-    with _on(stream):
-        if outputs is None:
-            (z, pz), (y, py) = _node_new(x, True), _node_new(x, True)
-        else:
-            z, y = outputs
-            pz, py = _node_row(z, "z", x), _node_row(y, "y", x)
-    _node_call(x.device, "tpconv_dropout_norm_forward", stream, plan._h, x.shape[0], px, pr, dropout.spec(x.device),
+    if outputs is None:
+        (z, pz), (y, py) = _node_new(x, True), _node_new(x, True)
+    else:
+        z, y = outputs
+        pz, py = _node_row(z, "z", x), _node_row(y, "y", x)
+    _node_call(x.device, "tpconv_dropout_norm_forward", plan._h, x.shape[0], px, pr, dropout.spec(x.device),
                pw, pb, pz, py)
     return z, y
 
@@ -691,21 +706,22 @@ def tpconv_dropout_norm_forward(plan, x, dropout, residual=None, weight=None, bi
 def tpconv_dropout_norm_backward(plan, z, weight, grad_y, dropout, grad_z=None, need_x=True, need_residual=True,
                                  need_weight=True, need_bias=True, ws=None, outputs=None, stream=None):
     """Returns (grad_x, grad_residual, grad_weight, grad_bias) from the stored z."""
+    if stream is not None:
+        return _on(tpconv_dropout_norm_backward, locals())
     dev, N, C, Cb = z.device, z.shape[0], plan.channels, plan.biases
     pz, pg, pgz = _node_x(plan, z, "z"), _node_row(grad_y, "grad_y", z), _node_row(grad_z, "grad_z", z)
     pw = _node_vec(weight, C, "weight", z)
-    with _on(stream):
-        if outputs is None:
-            gx, pgx = _node_new(z, need_x)
-            gr, pgr = _node_new(z, need_residual)
-            gw, pgw = _node_sums(weight, C, need_weight, dev)
-            gb, pgb = _node_sums(None, Cb, need_bias, dev)
-        else:
-            gx, gr, gw, gb = outputs
-            pgx, pgr = _node_row(gx, "grad_x", z), _node_row(gr, "grad_residual", z)
-            pgw, pgb = _node_vec(gw, C, "grad_weight", z), _node_vec(gb, Cb, "grad_bias", z)
-        ws, pws, nws = _node_ws(plan, N, ws, dev)
-    _node_call(dev, "tpconv_dropout_norm_backward", stream, plan._h, N, pz, pw, pg, pgz, dropout.spec(dev), pgx, pgr,
+    if outputs is None:
+        gx, pgx = _node_new(z, need_x)
+        gr, pgr = _node_new(z, need_residual)
+        gw, pgw = _node_sums(weight, C, need_weight, dev)
+        gb, pgb = _node_sums(None, Cb, need_bias, dev)
+    else:
+        gx, gr, gw, gb = outputs
+        pgx, pgr = _node_row(gx, "grad_x", z), _node_row(gr, "grad_residual", z)
+        pgw, pgb = _node_vec(gw, C, "grad_weight", z), _node_vec(gb, Cb, "grad_bias", z)
+    ws, pws, nws = _node_ws(plan, N, ws, dev)
+    _node_call(dev, "tpconv_dropout_norm_backward", plan._h, N, pz, pw, pg, pgz, dropout.spec(dev), pgx, pgr,
                pgw, pgb, pws, nws)
     return gx, gr, gw, gb
 

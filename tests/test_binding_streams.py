@@ -12,30 +12,36 @@ from equivariant_gnn_tensor_dst_b200 import binding as B
 
 
 class Side:
-    """Stands for a torch stream."""
-    cuda_stream = 77
+    """Stands for a torch stream (of the device that the tensors here are on)."""
+    cuda_stream, device_index, device = 77, -1, torch.device("cpu")
+
+
+class Made(list):
+    """Allocations of a call, (stream they are made on, elements); the stream that is current."""
+    current = None
 
 
 @pytest.fixture
 def made(monkeypatch):
-    """Allocations of a call: (stream they are made on, elements)."""
-    made, on = [], [None]
+    made = Made()
 
     @contextlib.contextmanager
     def enter(stream):
-        on.append(stream)
+        before, made.current = made.current, stream
         yield
-        on.pop()
+        made.current = before
 
     def recorded(f):
         def call(*a, **k):
             k.pop("device", None)
             t = f(*a, **k)
-            made.append((on[-1], t.numel()))
+            made.append((made.current, t.numel()))
             return t
         return call
 
     monkeypatch.setattr(torch.cuda, "stream", enter)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: Side.device_index)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 5)
     for name in ("empty", "empty_like", "zeros"):
         monkeypatch.setattr(torch, name, recorded(getattr(torch, name)))
     return made
@@ -47,7 +53,7 @@ def node(monkeypatch, made):
     streams = []
     plan = B.NodePlan("8x0e+8x1o")
     monkeypatch.setattr(B, "_node_x", lambda plan, x, name: x.data_ptr())
-    monkeypatch.setattr(B, "_node_call", lambda device, name, stream, *args: streams.append(stream))
+    monkeypatch.setattr(B, "_node_call", lambda device, name, *args: streams.append(made.current))
     monkeypatch.setattr(B.Dropout, "spec", lambda self, device: self._ref)
     x, w, b = torch.ones(3000, plan.dim), torch.ones(plan.channels), torch.ones(plan.biases)
     return plan, x, w, b, streams
@@ -77,25 +83,25 @@ def test_node_tensors_belong_to_the_stream(node, made, name):
 
 
 class Library:
-    """The library's host functions; compute calls are recorded by their stream (the last argument)."""
+    """The library's host functions; compute calls are recorded by the stream that is current."""
 
-    def __init__(self, real, streams):
-        self.real, self.streams = real, streams
+    def __init__(self, real, made, streams):
+        self.real, self.made, self.streams = real, made, streams
 
     def __getattr__(self, name):
-        if name.endswith("_workspace_bytes") or name.startswith("tpconv_plan"):
+        if name.endswith("_workspace_bytes") or name.startswith(("tpconv_plan", "tpconv_node_plan")):
             return getattr(self.real, name)
-        return lambda *args: self.streams.append(args[-1]) or 0
+        return lambda *args: self.streams.append(self.made.current) or 0
 
 
 @pytest.fixture
 def graph(monkeypatch, made):
     streams = []
     plan = B.Plan("4x0e+4x1o", 1, "4x0e+4x1o")
-    library = Library(B.lib(), streams)
+    library = Library(B.lib(), made, streams)
     monkeypatch.setattr(B, "lib", lambda: library)
     monkeypatch.setattr(B, "_need", lambda t, dtype, name: None)
-    monkeypatch.setattr(B, "_stream", lambda stream: stream)
+    monkeypatch.setattr(B, "_stream", lambda: None)
     n, e = 50, 400
     i32 = lambda *v: torch.ones(*v, dtype=torch.int32)
     a = dict(x=torch.ones(n, plan.dim_in), pos=torch.ones(n, 3), row_ptr=i32(n + 1), src=i32(e), t_ptr=i32(n + 1),
@@ -140,3 +146,29 @@ def test_gathered_rows_are_as_many_as_perm(graph, rows):
     with pytest.raises(ValueError):
         B.tpconv_gather_rows(a["x"], torch.ones(rows, dtype=torch.int32))
     assert not streams
+
+
+def test_current_stream_is_not_entered_again(graph, node, made, monkeypatch):
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: Side.cuda_stream)
+    plan, a, _ = graph
+    GRAPH_CALLS["forward"](plan, a, stream=Side())
+    node_plan, x, w, b, _ = node
+    NODE_CALLS["norm_backward"](node_plan, x, w, b, stream=Side())
+    assert made and all(s is None for s, _ in made)
+    made.clear()
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)   # current on a device that is not
+    side = Side()
+    GRAPH_CALLS["forward"](plan, a, stream=side)
+    assert made and all(s is side for s, _ in made)
+
+
+def test_stream_of_another_device_is_refused(graph, node):
+    plan, a, streams = graph
+    node_plan, x, w, b, node_streams = node
+    other = Side()
+    other.device_index, other.device = 1, torch.device("cuda:1")
+    with pytest.raises(ValueError, match="stream is on cuda:1, x on cpu"):
+        GRAPH_CALLS["forward"](plan, a, stream=other)
+    with pytest.raises(ValueError, match="stream is on cuda:1, x on cpu"):
+        NODE_CALLS["norm_forward"](node_plan, x, w, b, stream=other)
+    assert not streams and not node_streams
